@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "fa_internal.h"
+#include "serving.h"
 
 namespace {
 
@@ -185,6 +186,8 @@ fa_status_t record_error(fa_status_t status, const char* message) {
     return fail(status, "%s", message);
 }
 fa_status_t record_ok() { return ok(); }
+fa_status_t check_tensor_arg(const fa_tensor_t* t, const char* name) { return check_tensor(t, name); }
+int device_sm_count(int device) { return sm_count(device); }
 }  // namespace fa
 
 extern "C" {

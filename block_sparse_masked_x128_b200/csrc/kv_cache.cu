@@ -1,0 +1,229 @@
+// kv_cache.cu -- writing new keys and values into a paged cache, quantised, and reading
+// sequences back.
+//
+// A row is one token's D values of one head.  8-bit caches hold a code per value and one fp32
+// scale per row:
+//   s8     scale = max(rn(amax / 127), 2^-126), code = x / scale to the nearest even integer
+//   e4m3   scale = the smallest power of two >= 2^-126 with amax / scale <= 448, code = x / scale
+//          to the nearest even e4m3 value (the division is exact, so the code does not depend on
+//          the precision it is done in)
+// and a row that holds a NaN or an infinity gets scale = NaN, codes 0, and reads back as NaN.
+// 16-bit caches hold the rows as they are.  Reading gives code * scale rounded once.
+//
+// Both kernels are bound by HBM (append: 2 bytes read and 1 written a value and 4 a row).  A row
+// belongs to D / 8 lanes, 16 bytes of 16-bit values each, so its maximum is three or four
+// shuffles and nothing is staged; rows of k and v at the same place go together.
+#include "serving.h"
+#include "sm100_ptx.cuh"
+
+#include <cuda_fp16.h>
+
+namespace fa {
+namespace {
+
+__device__ int32_t g_cache_rows_status;   // 2: a page or position out of range was met
+
+constexpr int kRowThreads = 128;
+
+template <bool BF16>
+__device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            f[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)));
+            f[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+        }
+    }
+}
+
+// x / scale to the nearest integer, ties to even, exactly (|x / scale| <= 127 (1 + 2^-23)).
+// The product with the rounded inverse is within 2^-15 of x / scale; only where it falls that
+// near a half does the exact sign of x - (r +- 1/2) scale, one fma, decide.
+__device__ __forceinline__ int quantise_s8(float x, float scale, float inv) {
+    float r = rintf(x * inv);
+    if (fabsf(fmaf(x, inv, -r)) > 0.4999f) {
+        const float up = fmaf(-(r + 0.5f), scale, x), down = fmaf(-(r - 0.5f), scale, x);
+        const bool odd = ((int)r & 1) != 0;
+        if (up > 0.f || (up == 0.f && odd)) r += 1.f;
+        else if (down < 0.f || (down == 0.f && odd)) r -= 1.f;
+    }
+    return (int)r;
+}
+
+__device__ __forceinline__ uint32_t quantise_e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two e4m3 codes as floats (exact).
+__device__ __forceinline__ float2 value_e4m3x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return make_float2(__half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu))),
+                       __half2float(__ushort_as_half((unsigned short)(h >> 16))));
+}
+
+// The scale of a row from the bits of its largest magnitude.
+template <int DT>
+__device__ __forceinline__ float row_scale(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+    if constexpr (DT == FA_DTYPE_S8) return fmaxf(__fdiv_rn(__uint_as_float(amax_bits), 127.f), 1.17549435e-38f);
+    // 448 = 1.75 * 2^8: the exponent of amax, one more where its mantissa exceeds 1.75, less 8.
+    const int e = (int)((amax_bits + 0x1FFFFFu) >> 23) - 8;
+    return __uint_as_float((uint32_t)max(e, 1) << 23);
+}
+
+// Grid (ceil(S / rows), H, B).
+template <int DT, int D, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheRowsParams p) {
+    constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    const int sub = threadIdx.x % LPR;
+    const int s = blockIdx.x * RPC + threadIdx.x / LPR;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int count = p.limit ? min(__ldg(p.limit + b), p.S) : p.S;
+    int page = -1;
+    int64_t pos = 0;
+    if (s < count) {
+        pos = (p.start ? (int64_t)__ldg(p.start + b) : 0) + s;
+        page = pos < 0 ? -1 : cache_page(p.c, b, pos >> p.c.page_shift);
+        if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+    }
+    const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (page >= 0)
+            r = *reinterpret_cast<const uint4*>(p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8);
+        const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+        void* pool = w ? p.c.v : p.c.k;
+        if constexpr (!CacheType<DT>::k8) {
+            if (page >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) = r;
+        } else {
+            float x[8];
+            row_unpack<BF16>(r, x);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+            const float scale = row_scale<DT>(m);
+            uint32_t c[2] = {0u, 0u};
+            if (m < 0x7f800000u) {
+                const float inv = __frcp_rn(scale);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t two;
+                    if constexpr (DT == FA_DTYPE_S8)
+                        two = (uint32_t)(quantise_s8(x[2 * i], scale, inv) & 0xFF) |
+                              (uint32_t)(quantise_s8(x[2 * i + 1], scale, inv) & 0xFF) << 8;
+                    else
+                        two = quantise_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+                    c[i / 2] |= two << (16 * (i % 2));
+                }
+            }
+            if (page >= 0) {
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = make_uint2(c[0], c[1]);
+                if (sub == 0)
+                    (w ? p.c.v_scale : p.c.k_scale)[(int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] +
+                                                    (int64_t)row * p.c.scale_stride[2]] = scale;
+            }
+        }
+    }
+}
+
+// Rows start .. start + S - 1 of each sequence; those past its length are zero.
+template <int DT, int D, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
+    constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    const int sub = threadIdx.x % LPR;
+    const int s = blockIdx.x * RPC + threadIdx.x / LPR;
+    const int h = blockIdx.y, b = blockIdx.z;
+    if (s >= p.S) return;
+    const int64_t pos = (p.start ? (int64_t)__ldg(p.start + b) : 0) + s;
+    int page = -1;
+    if (pos >= 0 && pos < __ldg(p.limit + b)) {
+        page = cache_page(p.c, b, pos >> p.c.page_shift);
+        if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+    }
+    const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (page >= 0) {
+            const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+            const void* pool = w ? p.c.v : p.c.k;
+            if constexpr (!CacheType<DT>::k8) {
+                r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pool) + at);
+            } else {
+                const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + at);
+                const float scale = (w ? p.c.v_scale : p.c.k_scale)[(int64_t)page * p.c.scale_stride[0] +
+                                                                    h * p.c.scale_stride[1] +
+                                                                    (int64_t)row * p.c.scale_stride[2]];
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = ((i < 2 ? c.x : c.y) >> (16 * (i % 2))) & 0xFFFFu;
+                    float2 f;
+                    if constexpr (DT == FA_DTYPE_S8) f = make_float2((float)(int8_t)(two & 0xFF), (float)(int8_t)(two >> 8));
+                    else f = value_e4m3x2(two);
+                    o[i] = pack2<BF16>(f.x * scale, f.y * scale);
+                }
+                r = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        *reinterpret_cast<uint4*>(p.out[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8) = r;
+    }
+}
+
+template <int DT, int D, bool BF16>
+cudaError_t launch_rows(const CacheRowsParams& p, bool append, cudaStream_t st) {
+    constexpr int RPC = kRowThreads / (D / 8);
+    const dim3 grid((unsigned)((p.S + RPC - 1) / RPC), (unsigned)p.c.H, (unsigned)p.B);
+    if (append) cache_append_kernel<DT, D, BF16><<<grid, kRowThreads, 0, st>>>(p);
+    else cache_read_kernel<DT, D, BF16><<<grid, kRowThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_any(const CacheRowsParams& p, int dtype, int D, bool bf16, bool append, cudaStream_t st) {
+#define FA_ROWS(T, DD, BB) \
+    if (dtype == T && D == DD && bf16 == BB) return launch_rows<T, DD, BB>(p, append, st);
+#define FA_ROWS_D(T, BB) FA_ROWS(T, 64, BB) FA_ROWS(T, 128, BB)
+    FA_ROWS_D(FA_DTYPE_F16, false)
+    FA_ROWS_D(FA_DTYPE_BF16, true)
+    FA_ROWS_D(FA_DTYPE_E4M3, false)
+    FA_ROWS_D(FA_DTYPE_E4M3, true)
+    FA_ROWS_D(FA_DTYPE_S8, false)
+    FA_ROWS_D(FA_DTYPE_S8, true)
+#undef FA_ROWS_D
+#undef FA_ROWS
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheRowsParams& p, int dtype, int D, bool bf16, cudaStream_t st) {
+    return launch_any(p, dtype, D, bf16, true, st);
+}
+cudaError_t launch_cache_read(const CacheRowsParams& p, int dtype, int D, bool bf16, cudaStream_t st) {
+    return launch_any(p, dtype, D, bf16, false, st);
+}
+
+cudaError_t cache_rows_status(cudaStream_t st, int32_t* out) {
+    void* addr = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&addr, g_cache_rows_status);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyAsync(out, addr, 4, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *out != 0) {
+        e = cudaMemsetAsync(addr, 0, 4, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    return e;
+}
+
+}  // namespace fa

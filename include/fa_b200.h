@@ -68,6 +68,19 @@ typedef enum fa_status {
 
 #define FA_DTYPE_F16   0
 #define FA_DTYPE_BF16  1
+/* 8-bit types of a K/V cache, with one fp32 scale a row (fa_kv_cache_t only). */
+#define FA_DTYPE_E4M3  2
+#define FA_DTYPE_S8    3
+
+/* Which elements of a head's rotated part form a pair (fa_rotary). */
+#define FA_ROTARY_HALF         0   /* (i, i + rot_dim / 2) */
+#define FA_ROTARY_INTERLEAVED  1   /* (2i, 2i + 1)         */
+
+/* How rotary frequencies are scaled for contexts longer than the trained one. */
+#define FA_ROTARY_SCALE_NONE      0
+#define FA_ROTARY_SCALE_LINEAR    1   /* every frequency divided by factor */
+#define FA_ROTARY_SCALE_BASE      2   /* base times factor^(rot_dim / (rot_dim - 2)) */
+#define FA_ROTARY_SCALE_BY_PARTS  3   /* slow pairs divided by factor, fast pairs kept */
 
 typedef struct fa_mask_params {
     int32_t        window;                /* W > 0, used when FA_MASK_SLIDING_WINDOW is set        */
@@ -344,6 +357,133 @@ fa_status_t fa_masked_softmax(const fa_tensor_t* scores, uint32_t mask_kind, int
 /* Synchronise `stream`, read and clear the status word of the fa_masked_softmax kernels:
  * FA_OK, FA_ERR_TIMEOUT (a bounded wait ran out), or FA_ERR_CUDA. */
 fa_status_t fa_masked_softmax_status(void* stream);
+
+/*
+ * Rotary positions.
+ *
+ * fa_rotary_frequencies -- fill `frequencies` (HOST, rot_dim / 2 doubles) with the angle in
+ * radians that pair i turns a position: base^(-2i / rot_dim), scaled as `scaling` says (NULL or
+ * kind NONE: not at all).  BY_PARTS: a pair that makes r = original_len * f / 2 pi turns over the
+ * trained length keeps f for r >= high_turns, gets f / factor for r <= low_turns, and goes
+ * linearly in r between.  Host code only; copy the result to the device for fa_rotary.
+ */
+typedef struct fa_rotary_scaling {
+    int32_t kind;            /* FA_ROTARY_SCALE_*                        */
+    double  factor;          /* > 0                                      */
+    double  original_len;    /* BY_PARTS: trained length, > 0            */
+    double  low_turns;       /* BY_PARTS: 0 <= low_turns < high_turns    */
+    double  high_turns;
+} fa_rotary_scaling_t;
+fa_status_t fa_rotary_frequencies(int32_t rot_dim, double base, const fa_rotary_scaling_t* scaling,
+                                  double* frequencies);
+
+/*
+ * fa_rotary -- turn the pairs of q and k by their positions' angles, in one launch.
+ *
+ *   y1 = factor (x1 cos a - x2 sin a),  y2 = factor (x2 cos a + x1 sin a),  a = position * f_i
+ *
+ * for the pairs of the first rot_dim elements of each head (layout FA_ROTARY_HALF or
+ * INTERLEAVED); the other elements are copied.  inverse != 0 turns by -a: the gradient, with the
+ * outputs' gradients as inputs.  The angle is reduced to one turn exactly, so far positions are as
+ * accurate as near ones; the result is rounded once.
+ *
+ *   q            (B, Hq, S, D); k (B, Hk, S, D) of the same dtype, or NULL for q alone
+ *   positions    device int32 [B][position_stride], entry (b, s); position_stride 0 shares one row
+ *                among all sequences; NULL: position0 + s
+ *   frequencies  device double[rot_dim / 2], radians a position
+ *   rot_dim      even, 2 .. D
+ *   q_out, k_out shapes and dtype of q and k, caller-owned; may be q and k themselves with the
+ *                same strides, otherwise must not overlap the inputs.  k_out is NULL iff k is
+ *
+ * Supported: D a multiple of 8 up to 1024; fp16 or bf16.
+ */
+fa_status_t fa_rotary(const fa_tensor_t* q, const fa_tensor_t* k, const int32_t* positions,
+                      int64_t position_stride, int64_t position0, const double* frequencies,
+                      int32_t rot_dim, int32_t layout, float factor, int32_t inverse,
+                      fa_tensor_t* q_out, fa_tensor_t* k_out, void* stream);
+
+/*
+ * A paged K/V cache: caller-owned device pools of n_pages pages, each holding page_size
+ * consecutive tokens of one sequence for every kv head.  Element (page, head, row, d) of k and of
+ * v lies at page * stride[0] + head * stride[1] + row * stride[2] + d, so (n_pages, H, page_size,
+ * D) and (n_pages, page_size, H, D) pools both fit.
+ *
+ * 8-bit types hold codes and one fp32 scale a row, at (page, head, row) of k_scale and v_scale; a
+ * value is code * scale:
+ *   S8    scale = max(fp32(amax / 127), 2^-126), code = row / scale to the nearest even integer
+ *   E4M3  scale = the smallest power of two >= 2^-126 with amax / scale <= 448,
+ *         code = row / scale to the nearest even e4m3 value
+ * with amax the row's largest magnitude.  A row with a NaN or an infinity is written with scale
+ * NaN and codes 0.
+ */
+typedef struct fa_kv_cache {
+    void*   k;                 /* 16-byte aligned */
+    void*   v;
+    float*  k_scale;           /* 8-bit types; NULL otherwise */
+    float*  v_scale;
+    int32_t dtype;             /* FA_DTYPE_F16, BF16, E4M3 or S8 */
+    int32_t page_size;         /* a power of two, 16 .. 1024 */
+    int64_t n_pages, H, D;     /* D is 64 or 128 */
+    int64_t stride[3];         /* elements: page, head, row; positive multiples of 16 bytes */
+    int64_t scale_stride[3];   /* elements: page, head, row; positive */
+} fa_kv_cache_t;
+
+/*
+ * Shared by the calls on a cache:
+ *   page_table   device int32 [B][table_stride], of which table_width columns are valid: entry
+ *                (b, j) is the page of tokens j * page_size .. of sequence b.  Only the entries of
+ *                tokens that a call touches are read.
+ *   A page index outside [0, n_pages), a position outside [0, table_width * page_size) or a length
+ *   outside [0, table_width * page_size] is skipped (decode: clamped) and recorded:
+ *   fa_cache_status then returns FA_ERR_INVALID_ARG.
+ *   Two rows of one call must not go to the same place of the cache.
+ *
+ * fa_cache_append -- write the new rows k and v (B, H, S, D), fp16 or bf16 (a 16-bit cache's own
+ * dtype), of each sequence b at positions start[b] + s for s < count[b] (count NULL: all S rows),
+ * quantised for 8-bit caches.  Rows of a padded batch past count[b] are not read and nothing is
+ * written for them.  start and count are device int32 [B]; counts outside [0, S] are clamped.
+ */
+fa_status_t fa_cache_append(const fa_tensor_t* k, const fa_tensor_t* v, const fa_kv_cache_t* cache,
+                            const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                            const int32_t* start, const int32_t* count, void* stream);
+
+/*
+ * fa_cache_read -- positions start[b] .. start[b] + S - 1 (start NULL: from 0) of each sequence
+ * into k_out and v_out (B, H, S, D), fp16 or bf16 (a 16-bit cache's own dtype).  Positions at or
+ * past kv_lens[b] (device int32 [B]) come out as zeros, so the result can be attended to as it is.
+ */
+fa_status_t fa_cache_read(const fa_kv_cache_t* cache, const int32_t* page_table,
+                          int64_t table_stride, int64_t table_width, const int32_t* start,
+                          const int32_t* kv_lens, fa_tensor_t* k_out, fa_tensor_t* v_out, void* stream);
+
+/*
+ * fa_decode -- attention of one new token a sequence over a paged cache, heads in groups.
+ *
+ *   q           (B, HQ, 1, D), fp16 or bf16 (a 16-bit cache's own dtype); HQ a multiple of the
+ *               cache's H: query head h reads kv head h / (HQ / H)
+ *   kv_lens     device int32 [B]: the tokens of each sequence in the cache, the new one among
+ *               them; the query is at position kv_lens[b] - 1.  Read by the kernels, so one
+ *               captured call serves every length
+ *   window      0, or the number of last keys that are attended to
+ *   score_mod_kind, params, scale   as in fa_forward; ALiBi's slopes are per query head and its
+ *               distances kv - (kv_lens[b] - 1)
+ *   out         (B, HQ, 1, D), q's dtype; lse: device fp32 [B][HQ] or NULL
+ *   workspace   device scratch of fa_decode_workspace_bytes bytes, 16-byte aligned; nothing in it
+ *               outlives the call.  Calls that overlap on the GPU need distinct workspaces.
+ *
+ * A sequence of length 0 gets out = 0, lse = -inf and may have no pages.  Cache rows that are not
+ * attended to are not read.  Repeated calls give the same bits.
+ */
+size_t fa_decode_workspace_bytes(int64_t B, int64_t HQ, int64_t H, int64_t D);
+fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const int32_t* page_table,
+                      int64_t table_stride, int64_t table_width, const int32_t* kv_lens,
+                      int32_t window, uint32_t score_mod_kind, const fa_score_params_t* params,
+                      float scale, fa_tensor_t* out, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Synchronise `stream`, read and clear the status words of the calls on caches on the current
+ * device: FA_OK, FA_ERR_INVALID_ARG (a page, position or length was out of range), FA_ERR_CUDA. */
+fa_status_t fa_cache_status(void* stream);
 
 /* Fill `info` with the mask's extents and device pointers.  FA_ERR_INVALID_ARG on NULL. */
 fa_status_t fa_block_mask_get(const fa_block_mask_t* block_mask, fa_block_mask_info_t* info);

@@ -17,12 +17,15 @@ the pages (see each function's docstring for the passage it follows):
   attention_backward(q, k, v, dO, ...)          dQ, dK, dV of that definition
   masked_softmax(scores, offset)                causal select + softmax over
                                                 materialised scores (the unfused chain)
+  serving.rotary / quantise_* / decode          rotary positions, cache rows in 8 bits, and
+                                                attention of one token over cached rows
 
 Every function is pinned by a "not gpu" test against facts the pages or the
 mathematics fix; where a function follows a reading of the pages (the composition
 order of soft-cap and ALiBi, for one), the pin checks that reading.
 """
 from .backward import attention_backward, make_score_mod_grad, soft_cap_grad  # noqa: F401
+from . import serving  # noqa: F401
 from .masked_softmax import masked_softmax, causal_keep, finfo_min, BF16_MIN, FP16_MIN  # noqa: F401
 from .attention import (  # noqa: F401
     causal, sliding_window, document, sequence_lengths, conjunction, all_true, make_mask_mod,
