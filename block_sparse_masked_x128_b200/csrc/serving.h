@@ -69,7 +69,7 @@ struct CacheDecodeParams {
     int32_t B, HQ, group;         // group = query heads a kv head
     const int32_t* kv_lens;       // [B]
     int32_t window;               // 0: all keys
-    float scale_log2, softcap_log2, softcap_k;   // softcap_k: 2 log2(e) scale / softcap
+    float scale_log2, softcap_log2, softcap_k;   // softcap_k: 2 / softcap
     const float* alibi_slopes;
     int32_t score_kind;
     float* partials;

@@ -362,7 +362,7 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     p.window = window;
     p.scale_log2 = (float)(sc * log2e);
     p.softcap_log2 = (float)(cap * log2e);
-    p.softcap_k = (float)(2.0 * log2e * sc / cap);
+    p.softcap_k = (float)(2.0 / cap);
     p.alibi_slopes = params ? params->alibi_slopes : nullptr;
     p.score_kind = (int32_t)score_mod_kind;
     p.partials = static_cast<float*>(workspace);
