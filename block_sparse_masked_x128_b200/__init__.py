@@ -12,7 +12,9 @@ FlexAttention API the pages use ("How to Use FlexAttention on Apple Silicon", Se
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 # FA_B200_LIBRARY may name another build of the same library (build.py --debug writes
@@ -152,31 +154,22 @@ _lib.fa_backward.argtypes = [ctypes.POINTER(FaTensor)] * 5 + [
     ctypes.c_size_t, ctypes.c_void_p]
 _lib.fa_backward.restype = _status
 
-_lib.fa_rotary_frequencies.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.POINTER(FaRotaryScaling),
-                                       ctypes.c_void_p]
-_lib.fa_rotary_frequencies.restype = _status
-_lib.fa_rotary.argtypes = [
-    ctypes.POINTER(FaTensor), ctypes.POINTER(FaTensor), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
-    ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.POINTER(FaTensor),
-    ctypes.POINTER(FaTensor), ctypes.c_void_p]
-_lib.fa_rotary.restype = _status
-_lib.fa_cache_append.argtypes = [
-    ctypes.POINTER(FaTensor), ctypes.POINTER(FaTensor), ctypes.POINTER(FaKvCache), ctypes.c_void_p,
-    ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
-_lib.fa_cache_append.restype = _status
-_lib.fa_cache_read.argtypes = [
-    ctypes.POINTER(FaKvCache), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
-    ctypes.c_void_p, ctypes.POINTER(FaTensor), ctypes.POINTER(FaTensor), ctypes.c_void_p]
-_lib.fa_cache_read.restype = _status
-_lib.fa_decode_workspace_bytes.argtypes = [ctypes.c_int64] * 4
+# The serving calls take their descriptions (fa_tensor_t, fa_kv_cache_t, ...) as addresses: a packed
+# bytes object (_packed below) or a byref() alike.
+_p, _i64 = ctypes.c_void_p, ctypes.c_int64
+_lib.fa_rotary_frequencies.argtypes = [ctypes.c_int32, ctypes.c_double, _p, _p]
+_lib.fa_rotary.argtypes = [_p, _p, _p, _i64, _i64, _p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                           ctypes.c_int32, _p, _p, _p]
+_lib.fa_cache_append.argtypes = [_p, _p, _p, _p, _i64, _i64, _p, _p, _p]
+_lib.fa_cache_read.argtypes = [_p, _p, _i64, _i64, _p, _p, _p, _p, _p]
+_lib.fa_decode_workspace_bytes.argtypes = [_i64] * 4
+_lib.fa_decode.argtypes = [_p, _p, _p, _i64, _i64, _p, ctypes.c_int32, ctypes.c_uint32, _p, ctypes.c_float, _p, _p,
+                           _p, ctypes.c_size_t, _p]
+_lib.fa_cache_status.argtypes = [_p]
+for _f in (_lib.fa_rotary_frequencies, _lib.fa_rotary, _lib.fa_cache_append, _lib.fa_cache_read, _lib.fa_decode,
+           _lib.fa_cache_status):
+    _f.restype = _status
 _lib.fa_decode_workspace_bytes.restype = ctypes.c_size_t
-_lib.fa_decode.argtypes = [
-    ctypes.POINTER(FaTensor), ctypes.POINTER(FaKvCache), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
-    ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.POINTER(FaScoreParams), ctypes.c_float,
-    ctypes.POINTER(FaTensor), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
-_lib.fa_decode.restype = _status
-_lib.fa_cache_status.argtypes = [ctypes.c_void_p]
-_lib.fa_cache_status.restype = _status
 
 
 class FaError(RuntimeError):
@@ -589,20 +582,41 @@ def masked_softmax(scores, offset: Optional[int] = None, *, causal: bool = True,
 
 # ---------------------------------------------------------------- serving: rotary, cache, decode
 
-def _on(device, call):
-    """call() with `device` current."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        return call()
-    with torch.cuda.device(device):
-        return call()
+# These calls are short, a decode step has several, and the GPU waits for the host between them:
+# the descriptions are packed in one go (fa_tensor_t: address, dtype, padding, four extents, four
+# strides) and the current stream is asked for as a bare pointer.
+_packed_tensor = struct.Struct("=Qi4x8q").pack
 
 
-def _int32_rows(t, name: str, device, *shape):
-    """Raise ValueError unless t is an int32 CUDA tensor of that shape on `device`, contiguous."""
+def _packed(t) -> bytes:
+    """fa_tensor(t) as bytes."""
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError("expected a (B, H, S, D) tensor")
+    return _packed_tensor(t.data_ptr(), _dtype_code(t.dtype), *shape, *t.stride())
+
+
+def _call(name: str, device, stream, *args) -> None:
+    """_lib.name(*args, stream) with `device` current."""
     import torch
-    if not (t.dtype == torch.int32 and t.shape == shape and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    status = getattr(_lib, name)(*args, stream)
+    if status != FA_OK:
+        raise FaError(status, name)
+
+
+def _int32_rows(t, name: str, device, n: int):
+    """Raise ValueError unless t is a contiguous int32 CUDA tensor of n values on `device`."""
+    import torch
+    if not (t.dtype == torch.int32 and t.shape == (n,) and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape ({n},) on {device}")
     return t.data_ptr()
 
 
@@ -652,14 +666,9 @@ def rotary(q, k, positions, frequencies, *, interleaved: bool = False, factor: f
     for t, what in ((q_out, "q_out"), (k_out, "k_out")):
         if t is not None and t.device != dev:
             raise ValueError(f"{what} must be on q's device")
-
-    def call():
-        return _lib.fa_rotary(ctypes.byref(fa_tensor(q)), ctypes.byref(fa_tensor(k)) if k is not None else None, pos_ptr,
-                              pos_stride, pos0, frequencies.data_ptr(), 2 * frequencies.numel(),
-                              FA_ROTARY_INTERLEAVED if interleaved else FA_ROTARY_HALF, factor, 1 if inverse else 0,
-                              ctypes.byref(fa_tensor(q_out)), ctypes.byref(fa_tensor(k_out)) if k_out is not None else None,
-                              _stream_ptr(stream))
-    _check(_on(dev, call), "fa_rotary")
+    _call("fa_rotary", dev, stream, _packed(q), _packed(k) if k is not None else None, pos_ptr, pos_stride, pos0,
+          frequencies.data_ptr(), 2 * frequencies.numel(), FA_ROTARY_INTERLEAVED if interleaved else FA_ROTARY_HALF,
+          factor, 1 if inverse else 0, _packed(q_out), _packed(k_out) if k_out is not None else None)
     return q_out, k_out
 
 
@@ -733,8 +742,7 @@ def cache_append(cache: PagedKVCache, k, v, page_table, start, *, count=None, st
     table = cache._table(page_table, B)
     start_ptr = _int32_rows(start, "start", dev, B)
     count_ptr = _int32_rows(count, "count", dev, B) if count is not None else None
-    _check(_on(dev, lambda: _lib.fa_cache_append(ctypes.byref(fa_tensor(k)), ctypes.byref(fa_tensor(v)), cache._ref, *table,
-                                                 start_ptr, count_ptr, _stream_ptr(stream))), "fa_cache_append")
+    _call("fa_cache_append", dev, stream, _packed(k), _packed(v), cache._ref, *table, start_ptr, count_ptr)
 
 
 def cache_read(cache: PagedKVCache, page_table, kv_lens, S: int, *, start=None, dtype=None, k_out=None,
@@ -753,13 +761,19 @@ def cache_read(cache: PagedKVCache, page_table, kv_lens, S: int, *, start=None, 
     table = cache._table(page_table, B)
     lens_ptr = _int32_rows(kv_lens, "kv_lens", dev, B)
     start_ptr = _int32_rows(start, "start", dev, B) if start is not None else None
-    _check(_on(dev, lambda: _lib.fa_cache_read(cache._ref, *table, start_ptr, lens_ptr, ctypes.byref(fa_tensor(outs[0])),
-                                               ctypes.byref(fa_tensor(outs[1])), _stream_ptr(stream))), "fa_cache_read")
+    _call("fa_cache_read", dev, stream, cache._ref, *table, start_ptr, lens_ptr, _packed(outs[0]), _packed(outs[1]))
     return tuple(outs)
 
 
 def decode_workspace_bytes(B: int, HQ: int, H: int, D: int) -> int:
     return int(_lib.fa_decode_workspace_bytes(B, HQ, H, D))
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(device, B: int, HQ: int, H: int, D: int) -> int:
+    import torch
+    with torch.cuda.device(device):
+        return decode_workspace_bytes(B, HQ, H, D)
 
 
 def decode_attention(q, cache: PagedKVCache, page_table, kv_lens, *, window: int = 0,
@@ -785,17 +799,16 @@ def decode_attention(q, cache: PagedKVCache, page_table, kv_lens, *, window: int
         raise ValueError("lse must be a contiguous float32 tensor (B, HQ, 1) on the cache's device")
     table = cache._table(page_table, B)
     lens_ptr = _int32_rows(kv_lens, "kv_lens", dev, B)
-    params = FaScoreParams(float(softcap), _check_alibi(alibi_slopes, q))
-
-    def call():
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(decode_workspace_bytes(B, HQ, cache.H, cache.D), dtype=torch.uint8, device=dev)
-        return _lib.fa_decode(ctypes.byref(fa_tensor(q)), cache._ref, *table, lens_ptr, int(window), int(score_mod),
-                              ctypes.byref(params), float(scale) if scale is not None else -1.0,
-                              ctypes.byref(fa_tensor(out)), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
-                              ws.numel() * ws.element_size(), _stream_ptr(stream))
-    _check(_on(dev, call), "fa_decode")
+    params = None
+    if score_mod:
+        params = ctypes.byref(FaScoreParams(float(softcap), _check_alibi(alibi_slopes, q)))
+    if workspace is None:
+        workspace = torch.empty(_decode_workspace(dev, B, HQ, cache.H, cache.D), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError("workspace must be on the cache's device")
+    _call("fa_decode", dev, stream, _packed(q), cache._ref, *table, lens_ptr, window, score_mod, params,
+          scale if scale is not None else -1.0, _packed(out), lse.data_ptr() if lse is not None else None,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 

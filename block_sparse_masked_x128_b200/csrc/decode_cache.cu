@@ -6,27 +6,30 @@
 //
 // The work is reading K and V once, so HBM bounds it as long as nothing else is in the way:
 //
-//   Split      the keys of all (sequence, kv head)s form one list of units of kUnit keys, and the
-//              CTAs of one wave take equal shares of it, so ragged lengths and single long
-//              sequences load every SM alike.  The lengths are device data: each CTA finds its
-//              share by a scan over the sequences.  A share that holds all of a head's keys writes
-//              the result itself; otherwise its (m, l, O) goes to the workspace and the merge
-//              kernel joins the pieces in key order (no atomics: the same bits every time).
+//   Split      the keys of every (sequence, kv head) are cut into chunks of one size, chosen on the
+//              device from the lengths so that about kWaves times as many chunks as CTAs fit on
+//              the GPU come out; one CTA takes one chunk, and the block scheduler hands them out,
+//              so ragged lengths and single long sequences load every SM alike.  A head
+//              with one chunk is finished by its CTA; otherwise the chunk's (m, l, O) goes to the
+//              workspace and the merge kernel joins the chunks in key order (no atomics: the same
+//              bits every time).
 //   Heads      the query heads of a kv head are the columns of the products (8 or 16 at a time):
 //              S^T = K q^T and O^T = V^T P^T, with 16 keys or 16 dims as rows.  The matrix
 //              pipe is needed only because one cache byte meets up to 16 heads; at 8 columns
 //              mma.sync keeps up with HBM several times over, and its operands come straight
 //              from the loaded bytes.
-//   Loads      each lane copies with cp.async exactly the bytes that its own fragments are made
-//              of, into slots that only it reads (the products' contraction index may run through
-//              the dims in any order, so a lane's 16 contiguous bytes serve as four steps of it).
-//              So shared memory is a queue a lane: no barrier, no layout, no bank conflict.
+//   Loads      each warp has a ring of its own in shared memory, filled with cp.async and read back
+//              as fragments: the products' contraction index may run through the dims in any order,
+//              so 16 contiguous bytes of a row serve a lane for four steps of it, and nothing but
+//              the slots' order (below) is arranged.  No barrier between the warps.
 //   8 bits     codes become fp16 exactly, in registers.  The key's scale multiplies its score, the
-//              value's scale the weight p, both in fp32.  q is brought into fp16's range by a
-//              power of two a head, the weights by a running power of two R >= every v scale so
-//              far, so neither rounds out of range: q keeps all its bits, p is rounded to 11.
-//   Softmax    the reference m of a head's exponents is raised only when a score exceeds it by 8
-//              (in log2): weights stay below 2^8 and most tiles need no reduction over the lanes.
+//              value's scale the weight, both in fp32.  q is brought into fp16's range by a power of
+//              two a head, so it keeps all its bits.
+//   Softmax    a head's weights are w_j = 2^(x_j - m) vscale_j, rounded to 16 bits for the product
+//              (the sum of the 2^(x_j - m) is fp32).  The reference m is raised, to the largest
+//              x_j + log2 vscale_j so far, only when a weight exceeds 2^8: most tiles need no
+//              reduction over the lanes, and a weight is held to 2^-12 of itself or, in fp16, 2^-25
+//              of the largest, however the v scales differ.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -42,7 +45,12 @@ __device__ int32_t g_cache_decode_status;   // 2: a length or page out of range 
 constexpr int kCdWarps = 4, kCdThreads = 32 * kCdWarps;
 constexpr int kTileKeys = 16;               // keys a warp takes at a time
 constexpr float kCdLn2 = 0.6931471805599453f, kCdLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.f;               // how far (log2) a score may exceed the reference
+constexpr int kMinChunk = 2;                // units
+constexpr int kWaves = 3;                   // chunks aimed at, in CTAs that the GPU holds at once
+constexpr float kTopWeight = 256.f;         // weights above this raise the reference
+// Value scales below 2^-90 count as 2^-90 in the reference, which bounds 2^(x - m) by 2^98: the
+// sum over 2^25 keys stays finite.
+constexpr float kMinScaleLog2 = -90.f, kTopSum = 3.169126500570573e29f;
 
 template <int DT, int D, int NT>
 struct CdConfig {
@@ -51,24 +59,35 @@ struct CdConfig {
     static constexpr int kch = D * bytes / 64;            // 16-byte K chunks a lane and row
     static constexpr int vb = D / 8 * bytes < 16 ? 8 : 16;  // bytes of a V chunk
     static constexpr int vch = D / 8 * bytes / vb;        // V chunks a lane and row
+    static constexpr int lpr = D * bytes >= 128 ? 8 : 4;  // lanes that copy a row's line
+    // Copy j brings rows krow + k_row(j), and of a two-line row the line k_line(j).
+    static constexpr int lines = D * bytes == 256 ? 2 : 1;
+    static __device__ constexpr int k_row(int j) { return j / lines * (32 / lpr); }
+    static __device__ constexpr int k_line(int j) { return j % lines; }
+    static __device__ constexpr int k_dst(int j) { return (k_row(j) >> 3) * kch * 512 + (k_row(j) & 7) * 64 + k_line(j) * 1024; }
+    static __device__ constexpr int v_odd(int j) { return vb == 16 ? (j / lines) & 1 : 0; }
+    static __device__ constexpr int v_dst(int j) { return vb == 16 ? (j / lines >> 1) * 2 * vch * 512 + k_line(j) * 512 : j * 512; }
+    static constexpr int copies = 2 * kch;                // of 512 bytes, a tile's K or V
     static constexpr int kbytes = 2 * kch * 512;          // 2 rows a lane
     static constexpr int vbytes = 4 * vch * 32 * vb;      // 4 rows a lane
-    static constexpr int stage = kbytes + vbytes + (k8 ? 128 : 0);
-    static constexpr int occ = D * bytes == 256 ? 2 : (NT == 1 ? 4 : 3);
-    static constexpr int stages = D * bytes == 64 ? 6 : 3;
+    static constexpr int tile = kbytes + vbytes + (k8 ? 128 : 0);
+    // Tiles a warp works on at once: two independent chains of products and half the loop's
+    // overhead, where the ring has room for it.
+    static constexpr int sub = D * bytes == 256 ? 1 : 2;
+    static constexpr int stage = sub * tile;
+    static constexpr int occ = D * bytes == 256 ? (NT == 1 ? 3 : 2) : 3;
+    static constexpr int stages = D * bytes == 256 ? (NT == 1 ? 2 : 3) : (D * bytes == 128 ? 2 : 4);
     static constexpr int ring = kCdWarps * stages * stage;
+    static constexpr int unit = kCdWarps * sub;           // tiles of a unit
     // Join of the warps: O rows of D floats, 4 more after each 8 or 16 (bank conflicts).
     static constexpr int seg = k8 && D == 128 ? 16 : 8;
     static constexpr int orow = D + D / seg * 4;
-    static constexpr int join = kCdWarps * 8 * NT * (orow + 2) * 4 + 8 * NT * (kCdWarps + 2) * 4;
+    static constexpr int join = 8 * NT * (kCdWarps * (orow + 3) + 2) * 4;
     static constexpr int smem = ring > join ? ring : join;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -130,10 +149,11 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
 
 // The keys of sequence b that are attended to, [lo, len), and their number of units.
 struct SeqRange {
-    int32_t lo, len, tile0, tile1;
+    int32_t lo, len, tile0, tile1;       // tiles of 16 keys
     int32_t units;
 };
-__device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b) {
+// `unit`: tiles of a unit.
+__device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int unit) {
     SeqRange r;
     const int64_t cap = min((int64_t)p.c.table_width << p.c.page_shift, (int64_t)0x7fffffc0);
     const int n = __ldg(p.kv_lens + b);
@@ -142,43 +162,71 @@ __device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b)
     r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
     r.tile0 = r.lo / kTileKeys;
     r.tile1 = (r.len + kTileKeys - 1) / kTileKeys;
-    r.units = r.len > r.lo ? (r.tile1 - r.tile0 + kCdWarps - 1) / kCdWarps : 0;
+    r.units = r.len > r.lo ? (r.tile1 - r.tile0 + unit - 1) / unit : 0;
     return r;
 }
 
-// Scan over the sequences: the units of all of them, and those before thread t's own share
-// [t n, (t + 1) n) of the sequences.
-struct SeqScan {
-    int64_t total, before;
+// How the sequences are cut.  Chunk i of the grid is, in order, (sequence, kv head, piece, column
+// block); a sequence has ceil(units / chunk) pieces a head.  Heads of more than one piece have
+// workspace slots, in the same order: at most 2 kWaves ctas of them, since such a head has at most
+// 2 units / chunk pieces.
+struct Cut {
+    int32_t chunk;              // units a chunk
+    int64_t before, slot;       // chunks and slots before thread t's sequences [first, last)
+    int64_t total;              // chunks of all sequences
     int32_t first, last;
 };
 template <int THREADS>
-__device__ __forceinline__ SeqScan scan_sequences(const CacheDecodeParams& p) {
-    __shared__ int64_t sums[THREADS / 32];
+__device__ __forceinline__ Cut cut_sequences(const CacheDecodeParams& p, int HR, int unit) {
+    __shared__ int64_t sums[2][THREADS / 32], slots[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = (p.B + THREADS - 1) / THREADS;
-    SeqScan s;
-    s.first = min(p.B, (int)threadIdx.x * n);
-    s.last = min(p.B, s.first + n);
-    int64_t mine = 0;
-    for (int b = s.first; b < s.last; ++b) mine += seq_range(p, b).units;
-    int64_t inc = mine;
+    Cut c;
+    c.first = min(p.B, (int)threadIdx.x * n);
+    c.last = min(p.B, c.first + n);
+    int64_t units = 0;
+    for (int b = c.first; b < c.last; ++b) units += seq_range(p, b, unit).units;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(kFullMask, units, off);
+    if (lane == 0) sums[0][warp] = units;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) all += sums[0][w];
+    all *= HR;
+    c.chunk = (int32_t)max((int64_t)kMinChunk, (all + p.target_chunks - 1) / p.target_chunks);
+    int64_t mine = 0, held = 0;
+    for (int b = c.first; b < c.last; ++b) {
+        const int pieces = (seq_range(p, b, unit).units + c.chunk - 1) / c.chunk;
+        mine += (int64_t)pieces * HR;
+        held += pieces > 1 ? (int64_t)pieces * HR : 0;
+    }
+    int64_t inc = mine, hinc = held;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(kFullMask, inc, off);
-        if (lane >= off) inc += v;
+        const int64_t v = __shfl_up_sync(kFullMask, inc, off), h = __shfl_up_sync(kFullMask, hinc, off);
+        if (lane >= off) {
+            inc += v;
+            hinc += h;
+        }
     }
-    if (lane == 31) sums[warp] = inc;
+    if (lane == 31) {
+        sums[1][warp] = inc;
+        slots[warp] = hinc;
+    }
     __syncthreads();
-    int64_t below = 0, all = 0;
+    c.before = inc - mine;
+    c.slot = hinc - held;
+    c.total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) below += sums[w];
-        all += sums[w];
+        if (w < warp) {
+            c.before += sums[1][w];
+            c.slot += slots[w];
+        }
+        c.total += sums[1][w];
     }
-    s.total = all;
-    s.before = below + inc - mine;
-    return s;
+    return c;
 }
 
 // The head groups of a kv head: columns of the products, `rows` of them at a time.
@@ -192,51 +240,73 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     constexpr int KS = D / 16;                      // contraction steps of K q^T, and row tiles of O^T
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_before;
+    __shared__ int64_t s_index, s_slot;
     __shared__ int32_t s_seq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
 
-    // This CTA's share of the units, and where it begins.
+    // This CTA's chunk.
     const int CB = col_blocks(p.group, COLS), HR = p.c.H * CB;
-    const SeqScan scan = scan_sequences<kCdThreads>(p);
-    const int64_t total = scan.total * HR;
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u_begin = share * blockIdx.x, u_end = min(total, u_begin + share);
-    if (u_begin >= u_end) return;
+    const Cut cut = cut_sequences<kCdThreads>(p, HR, C::unit);
+    if ((int64_t)blockIdx.x >= cut.total) return;
     {
-        const int64_t q0 = u_begin / HR;
-        int64_t before = scan.before;
-        for (int b = scan.first; b < scan.last; ++b) {
-            const int n = seq_range(p, b).units;
-            if (q0 >= before && q0 < before + n) {
+        int64_t before = cut.before, slot = cut.slot;
+        for (int b = cut.first; b < cut.last; ++b) {
+            const int pieces = (seq_range(p, b, C::unit).units + cut.chunk - 1) / cut.chunk;
+            const int64_t n = (int64_t)pieces * HR;
+            if ((int64_t)blockIdx.x >= before && (int64_t)blockIdx.x < before + n) {
                 s_seq = b;
-                s_before = before;
+                s_index = (int64_t)blockIdx.x - before;
+                s_slot = slot;
             }
             before += n;
+            slot += pieces > 1 ? n : 0;
         }
     }
     __syncthreads();
-    int b = s_seq;
-    SeqRange sr = seq_range(p, b);
-    int64_t u = u_begin;
-    int hr, unit0;      // head group and first unit of the segment at hand
-    {
-        const int64_t rem = u_begin - s_before * HR;
-        hr = (int)(rem / sr.units);
-        unit0 = (int)(rem % sr.units);
-    }
+    const int b = s_seq;
+    const SeqRange sr = seq_range(p, b, C::unit);
+    const int index = (int)s_index, pieces = (sr.units + cut.chunk - 1) / cut.chunk;
+    const int cb = index % CB, piece = index / CB % pieces, h = index / CB / pieces;
+    const int col0 = cb * COLS, cols = min(COLS, p.group - col0), hq0 = h * p.group + col0;
+    const int unit0 = piece * cut.chunk, seg_units = min(cut.chunk, sr.units - unit0);
+    const bool complete = pieces == 1;
+
     const uint32_t ring = smem_u32(smem) + warp * C::stages * C::stage;
     const int64_t kv_row = p.c.stride[2] * C::bytes;
-    // Offsets of this lane's bytes within a tile: K rows r and r + 8, V rows 2c, 2c+1, 2c+8, 2c+9.
-    const int64_t k_off = r * kv_row + c * 16;
-    const int64_t v_off = 2 * c * kv_row + r * C::vb;
+    // Copies go by whole 128-byte lines, eight consecutive lanes a line (a 64-byte row: four), into
+    // the slots of the lanes whose fragments the bytes are.  The slots' order makes the writes and
+    // the reads of each quarter warp hit all banks once; with lanes of a line apart, or slots in
+    // plain lane order, the copies alone ran at 5.4 TB/s instead of 7.3.
+    const int krow = lane / C::lpr, kpiece = lane % C::lpr;
+    const int64_t lane_off = h * p.c.stride[1] * C::bytes + krow * kv_row + kpiece * 16;
+    const uint8_t* k_lane = static_cast<const uint8_t*>(p.c.k) + lane_off;
+    const uint8_t* v_lane = static_cast<const uint8_t*>(p.c.v) + lane_off;
+    // K: chunk e of rows r, r + 8 at lane (r ^ (e & 1), c)'s place.
+    const uint32_t k_slot = (kpiece >> 2) * 512 + ((krow ^ (kpiece >> 2)) * 4 + (kpiece & 3)) * 16;
+    // V: 16 bytes of row 2c at place 8 c + (r ^ 2c), for even and odd copies; 8 bytes at 16-byte
+    // place 4 (c ^ odd row) + (r / 2 ^ 2 (c / 2)).
+    uint32_t v_slot[2], v_read[2];
+    if constexpr (C::vb == 16) {
+        const int cl = lane >> 4;
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd)
+            v_slot[odd] = ((lane >> 3) & 1) * C::vch * 512 + (2 * odd + cl) * 128 + (kpiece ^ (2 * cl) ^ (4 * odd)) * 16;
+        v_read[0] = v_read[1] = (c * 8 + (r ^ (2 * c))) * 16;
+    } else {
+        const int odd = (lane >> 2) & 1;
+        v_slot[0] = odd * 256 + ((lane >> 3) ^ odd) * 64 + (kpiece ^ (2 * (lane >> 4))) * 16;
+        v_slot[1] = v_slot[0];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v_read[i] = (c ^ i) * 64 + ((r >> 1) ^ (2 * (c >> 1))) * 16 + (r & 1) * 8;
+    }
+    const uint32_t s_slot_of_lane = (lane & 7) * 16 + (lane >> 3) * 4;     // of row r: K r, K r + 8, V r, V r + 8
+    const float* s_lane = lane < 16 ? p.c.k_scale : p.c.v_scale;      // lanes 0-15 K scales, 16-31 V scales
+    if constexpr (C::k8) s_lane += h * p.c.scale_stride[1] + (lane & 15) * p.c.scale_stride[2];
+    const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
+    const int64_t page_bytes = p.c.stride[0] * C::bytes;
+    const int page_mask = (1 << p.c.page_shift) - 1;
 
-    while (u < u_end) {
-        const int seg_units = (int)min((int64_t)(sr.units - unit0), u_end - u);
-        const int h = hr / CB, col0 = (hr - h * CB) * COLS;
-        const int cols = min(COLS, p.group - col0);
-        const int hq0 = h * p.group + col0;
-
+    {
         // q as the second operand: lane (r, c) holds column r's dims of step s at
         // (16-byte chunk of 64 bytes of a K row) + 4 (step within the chunk) + 0..3.
         uint32_t qf[NT][KS][2];
@@ -302,59 +372,60 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
             for (int t = 0; t < KS; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
         }
-        float R = C::k8 ? 1.17549435e-38f : 1.f, inv_R = 8.50705917e37f;    // 2^-126 and 2^126; unused for 16 bits
-
-        const int t_end = min(sr.tile1, sr.tile0 + (unit0 + seg_units) * kCdWarps);
-        int t = sr.tile0 + unit0 * kCdWarps + warp;           // tile at hand
-        int ti = t;                                           // next tile to load
-        uint32_t bad = 0;                                     // ring slots whose page is out of range
-        auto page_of = [&](int tile) { return tile < t_end ? cache_page(p.c, b, ((int64_t)tile * kTileKeys) >> p.c.page_shift) : -1; };
-        int page = page_of(ti);
-        auto issue = [&](int slot) {
-            const int key0 = ti * kTileKeys;
-            if (page < 0) {
-                bad |= 1u << slot;
-                if (lane == 0) g_cache_decode_status = 2;
+        // Steps of `sub` tiles: this warp's are its own of each unit.
+        const int t_end = min(sr.tile1, sr.tile0 + (unit0 + seg_units) * C::unit);
+        int t = sr.tile0 + unit0 * C::unit + warp * C::sub;   // first tile of the step at hand
+        int ti = t;                                           // first tile of the next step to load
+        uint32_t bad = 0;                                     // tiles of the ring whose page is out of range
+        // Pages are looked up one step ahead of their use.
+        int page[C::sub];
+        auto look_up = [&]() {
+#pragma unroll
+            for (int u = 0; u < C::sub; ++u)
+                page[u] = ti + u < t_end ? __ldg(table + (((ti + u) * kTileKeys) >> p.c.page_shift)) : 0;
+        };
+        look_up();
+        auto issue_tile = [&](uint32_t st, int tile, int pg, uint32_t bit) {
+            const int key0 = tile * kTileKeys, row0 = key0 & page_mask;
+            const uint32_t ks = st + k_slot, vs = st + C::kbytes, ss = st + C::kbytes + C::vbytes + s_slot_of_lane;
+            const bool good = (unsigned)pg < (unsigned)p.c.n_pages;
+            const int64_t at = pg * page_bytes + row0 * kv_row;
+            const uint8_t *kp = k_lane + at, *vp = v_lane + at;
+            const float* sp = s_lane;
+            if constexpr (C::k8) sp += pg * p.c.scale_stride[0] + row0 * p.c.scale_stride[2];
+            if (good && key0 >= sr.lo && key0 + kTileKeys <= sr.len) {
+                bad &= ~bit;
+#pragma unroll
+                for (int j = 0; j < C::copies; ++j) cp_async16(ks + C::k_dst(j), kp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
+#pragma unroll
+                for (int j = 0; j < C::copies; ++j)
+                    cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), vp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
+                if constexpr (C::k8) cp_async4(ss, sp, 4);
             } else {
-                bad &= ~(1u << slot);
-            }
-            const bool whole = page >= 0 && key0 >= sr.lo && key0 + kTileKeys <= sr.len;
-            // Rows outside [lo, len) are filled with zeros, not read.
-            auto live = [&](int row) { return whole || (page >= 0 && key0 + row >= sr.lo && key0 + row < sr.len); };
-            const int row0 = key0 & ((1 << p.c.page_shift) - 1);
-            const int64_t at = page < 0 ? 0 : ((int64_t)page * p.c.stride[0] + h * p.c.stride[1]) * C::bytes + row0 * kv_row;
-            const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + at + k_off;
-            const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + at + v_off;
-            const uint32_t ks = ring + slot * C::stage + lane * 16;
+                // Rows outside [lo, len), and a page outside the pool, are filled with zeros, not read.
+                const bool any = tile < t_end;
+                if (any && !good && lane == 0) g_cache_decode_status = 2;
+                bad = good ? bad & ~bit : bad | bit;
+                auto live = [&](int row) { return any && good && key0 + row >= sr.lo && key0 + row < sr.len; };
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool ok = live(r + 8 * i);
-                const uint8_t* src = ok ? kp + 8 * i * kv_row : static_cast<const uint8_t*>(p.c.k);
-#pragma unroll
-                for (int e = 0; e < C::kch; ++e) cp_async16(ks + (i * C::kch + e) * 512, ok ? src + 64 * e : src, ok ? 16 : 0);
-            }
-            const uint32_t vs = ring + slot * C::stage + C::kbytes + lane * C::vb;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (i & 1) + 8 * (i >> 1);
-                const bool ok = live(2 * c + row);
-                const uint8_t* src = ok ? vp + row * kv_row : static_cast<const uint8_t*>(p.c.v);
-#pragma unroll
-                for (int e = 0; e < C::vch; ++e) {
-                    const uint32_t dst = vs + (i * C::vch + e) * 32 * C::vb;
-                    if constexpr (C::vb == 16) cp_async16(dst, ok ? src + 128 * e : src, ok ? 16 : 0);
-                    else cp_async8(dst, src, ok ? 8 : 0);
+                for (int j = 0; j < C::copies; ++j) {
+                    const bool ok = live(krow + C::k_row(j));
+                    const int64_t off = C::k_row(j) * kv_row + C::k_line(j) * 128;
+                    cp_async16(ks + C::k_dst(j), ok ? kp + off : k_lane, ok ? 16 : 0);
+                    cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), ok ? vp + off : v_lane, ok ? 16 : 0);
+                }
+                if constexpr (C::k8) {
+                    const bool ok = live(lane & 15);
+                    cp_async4(ss, ok ? sp : s_lane, ok ? 4 : 0);
                 }
             }
-            if constexpr (C::k8) {
-                // Lanes 0-15 the K scales, 16-31 the V scales.
-                const bool ok = live(lane & 15);
-                const float* sp = lane < 16 ? p.c.k_scale : p.c.v_scale;
-                if (ok) sp += (int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)(row0 + (lane & 15)) * p.c.scale_stride[2];
-                cp_async4(ring + slot * C::stage + C::kbytes + C::vbytes + lane * 4, sp, ok ? 4 : 0);
-            }
-            ti += kCdWarps;
-            page = page_of(ti);
+        };
+        auto issue = [&](int slot) {
+#pragma unroll
+            for (int u = 0; u < C::sub; ++u)
+                issue_tile(ring + slot * C::stage + u * C::tile, ti + u, page[u], 1u << (slot * C::sub + u));
+            ti += C::unit;
+            look_up();
         };
 #pragma unroll
         for (int s = 0; s < C::stages - 1; ++s) {
@@ -362,177 +433,185 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             cp_async_commit();
         }
         int slot = 0;
-        for (; t < t_end; t += kCdWarps) {
+        for (; t < t_end; t += C::unit) {
             cp_async_wait<C::stages - 2>();
-            __syncwarp();       // the scales come from other lanes; and all lanes are done with the last slot
+            __syncwarp();       // other lanes' copies have landed too; and all lanes are done with the last slot
             if (ti < t_end) issue(slot == 0 ? C::stages - 1 : slot - 1);
             cp_async_commit();
             const uint32_t st = ring + slot * C::stage;
 
-            // S^T: 16 keys x columns, in two halves of the contraction.
-            float acc[NT][2][4];
+            // S^T: 16 keys x columns a tile; with one tile in two halves of the contraction.
+            constexpr int CHAINS = C::sub == 1 ? 2 : 1;
+            float x[C::sub][NT][4], vscale[C::sub][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < C::sub; ++u) {
+                const uint32_t su = st + u * C::tile;
+                float acc[NT][CHAINS][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nt][0][i] = acc[nt][1][i] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < C::kch; ++e) {
-                const uint4 x = lds128(st + e * 512 + lane * 16), y = lds128(st + (C::kch + e) * 512 + lane * 16);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-                if constexpr (C::k8) {
+                    for (int k = 0; k < CHAINS; ++k) acc[nt][k][0] = acc[nt][k][1] = acc[nt][k][2] = acc[nt][k][3] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = codes_to_half2<DT, 0>(xw[i]), a1 = codes_to_half2<DT, 0>(yw[i]);
-                        const uint32_t a2 = codes_to_half2<DT, 1>(xw[i]), a3 = codes_to_half2<DT, 1>(yw[i]);
+                for (int e = 0; e < C::kch; ++e) {
+                    const uint32_t at = su + e * 512 + (lane * 16 ^ (e & 1) * 64);
+                    const uint4 v0 = lds128(at), v1 = lds128(at + C::kch * 512);
+                    const uint32_t xw[4] = {v0.x, v0.y, v0.z, v0.w}, yw[4] = {v1.x, v1.y, v1.z, v1.w};
+                    if constexpr (C::k8) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<false>(acc[nt][i & 1], a0, a1, a2, a3, qf[nt][4 * e + i][0], qf[nt][4 * e + i][1]);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = codes_to_half2<DT, 0>(xw[i]), a1 = codes_to_half2<DT, 0>(yw[i]);
+                            const uint32_t a2 = codes_to_half2<DT, 1>(xw[i]), a3 = codes_to_half2<DT, 1>(yw[i]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(acc[nt][i % CHAINS], a0, a1, a2, a3, qf[nt][4 * e + i][0], qf[nt][4 * e + i][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<BF16>(acc[nt][i % CHAINS], xw[2 * i], yw[2 * i], xw[2 * i + 1], yw[2 * i + 1], qf[nt][2 * e + i][0], qf[nt][2 * e + i][1]);
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<BF16>(acc[nt][i], xw[2 * i], yw[2 * i], xw[2 * i + 1], yw[2 * i + 1], qf[nt][2 * e + i][0], qf[nt][2 * e + i][1]);
                 }
-            }
-            float kscale[2] = {1.f, 1.f}, vscale[2] = {1.f, 1.f};
-            if constexpr (C::k8) {
-                const uint32_t ss = st + C::kbytes + C::vbytes + r * 4;
-                kscale[0] = lds_f32(ss);
-                kscale[1] = lds_f32(ss + 32);
-                vscale[0] = lds_f32(ss + 64);
-                vscale[1] = lds_f32(ss + 96);
-            }
-            // Scores in log2 units; x[nt][2 i + j]: key r + 8 i, column 2c + j.
-            float x[NT][4];
-            const int key = t * kTileKeys + r;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float s = acc[nt][0][i] + acc[nt][1][i];
-                    if constexpr (C::k8) s *= kscale[i >> 1];
-                    x[nt][i] = s * cs[nt][i & 1];
+                // Scores in log2 units; x[2 i + j]: key r + 8 i, column 2c + j.
+                float kscale[2] = {1.f, 1.f};
+                if constexpr (C::k8) {
+                    const uint4 s4 = lds128(su + C::kbytes + C::vbytes + r * 16);
+                    kscale[0] = __uint_as_float(s4.x), kscale[1] = __uint_as_float(s4.y);
+                    vscale[u][0] = __uint_as_float(s4.z), vscale[u][1] = __uint_as_float(s4.w);
                 }
-            if (p.score_kind != 0) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        // cap tanh(y) = cap (1 - 2 / (e^2y + 1)); softcap_k takes x to 2 y log2 e.
-                        if (p.score_kind & FA_SCORE_SOFTCAP) {
-                            const float y = x[nt][i] * p.softcap_k;
-                            x[nt][i] = p.softcap_log2 * (1.f - __fdividef(2.f, ex2_approx(y > 120.f ? 120.f : y) + 1.f));
-                        }
-                        if (p.score_kind & FA_SCORE_ALIBI)
-                            x[nt][i] = fmaf(slope[nt][i & 1], (float)(key + 8 * (i >> 1) - (sr.len - 1)), x[nt][i]);
+                        float s = acc[nt][0][i];
+                        if constexpr (CHAINS == 2) s += acc[nt][1][i];
+                        if constexpr (C::k8) s *= kscale[i >> 1];
+                        x[u][nt][i] = s * cs[nt][i & 1];
                     }
-            }
-            if (((bad >> slot) & 1u) || t * kTileKeys < sr.lo || (t + 1) * kTileKeys > sr.len) {
+                const int key = (t + u) * kTileKeys + r;
+                if (p.score_kind != 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int k = key + 8 * i;
-                    if (((bad >> slot) & 1u) || k < sr.lo || k >= sr.len)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) x[nt][2 * i] = x[nt][2 * i + 1] = -INFINITY;
+                        for (int i = 0; i < 4; ++i) {
+                            // cap tanh(y) = cap (1 - 2 / (e^2y + 1)); softcap_k takes x to 2 y log2 e.
+                            if (p.score_kind & FA_SCORE_SOFTCAP) {
+                                const float y = x[u][nt][i] * p.softcap_k;
+                                x[u][nt][i] = p.softcap_log2 * (1.f - __fdividef(2.f, ex2_approx(y > 120.f ? 120.f : y) + 1.f));
+                            }
+                            if (p.score_kind & FA_SCORE_ALIBI)
+                                x[u][nt][i] = fmaf(slope[nt][i & 1], (float)(key + 8 * (i >> 1) - (sr.len - 1)), x[u][nt][i]);
+                        }
+                }
+                const bool lost = (bad >> (slot * C::sub + u)) & 1u;
+                if (lost || (t + u) * kTileKeys < sr.lo || (t + u + 1) * kTileKeys > sr.len) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = key + 8 * i;
+                        if (lost || k < sr.lo || k >= sr.len)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) x[u][nt][2 * i] = x[u][nt][2 * i + 1] = -INFINITY;
+                    }
                 }
             }
-            bool raise = false;
+            // Weights against the present reference; one that is too large raises it first.
+            float w[C::sub][NT][4], e2[C::sub][NT][4];
+            auto weights = [&]() {
+                bool high = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int u = 0; u < C::sub; ++u)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) raise = raise || fmaxf(x[nt][j], x[nt][2 + j]) > m[nt][j] + kRaise;
-            float vtop = 0.f;
-            if constexpr (C::k8) {
-                vtop = fmaxf(fabsf(vscale[0]), fabsf(vscale[1]));
-                raise = raise || vtop > R;
-            }
-            if (__any_sync(kFullMask, raise)) {
-                float beta = 1.f;
-                if constexpr (C::k8) {
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(kFullMask, vtop, off));
-                    const uint32_t up = min((__float_as_uint(vtop) + 0x7fffffu) & 0x7f800000u, 0x7e800000u);   // at most 2^126
-                    const float Rn = fmaxf(R, __uint_as_float(up));
-                    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(Rn));
-                    beta = R * inv;
-                    R = Rn;
-                    inv_R = inv;
-                }
+                        for (int i = 0; i < 4; ++i) {
+                            const float e = ex2_approx(x[u][nt][i] - m[nt][i & 1]);
+                            e2[u][nt][i] = e;
+                            w[u][nt][i] = C::k8 ? e * vscale[u][i >> 1] : e;
+                            high = high || fabsf(w[u][nt][i]) > kTopWeight || (C::k8 && e > kTopSum);
+                        }
+                return high;
+            };
+            if (__any_sync(kFullMask, weights())) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = fmaxf(x[nt][j], x[nt][2 + j]);
+                        float top = m[nt][j];
+#pragma unroll
+                        for (int u = 0; u < C::sub; ++u)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float y = x[u][nt][2 * i + j];
+                                if constexpr (C::k8) y += fmaxf(__log2f(fabsf(vscale[u][i])), kMinScaleLog2);
+                                top = fmaxf(top, y);
+                            }
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
-                        const float mn = fmaxf(m[nt][j], top);
-                        const float alpha = ex2_approx(m[nt][j] - mn);
-                        m[nt][j] = mn;
+                        const float alpha = ex2_approx(m[nt][j] - top);
+                        m[nt][j] = top;
                         l[nt][j] *= alpha;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
-                            o[nt][k][j] *= alpha * beta;
-                            o[nt][k][2 + j] *= alpha * beta;
+                            o[nt][k][j] *= alpha;
+                            o[nt][k][2 + j] *= alpha;
                         }
                     }
+                weights();
             }
-            // Weights, and their transpose as the second operand.
-            uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < C::sub; ++u) {
+                // The weights' transpose is the second operand.
+                uint32_t pb[NT][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float w0 = ex2_approx(x[nt][2 * i] - m[nt][0]), w1 = ex2_approx(x[nt][2 * i + 1] - m[nt][1]);
-                    l[nt][0] += w0;
-                    l[nt][1] += w1;
-                    if constexpr (C::k8) {
-                        const float f = vscale[i] * inv_R;
-                        w0 *= f;
-                        w1 *= f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        l[nt][0] += e2[u][nt][2 * i];
+                        l[nt][1] += e2[u][nt][2 * i + 1];
+                        pb[nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i], w[u][nt][2 * i + 1]));
                     }
-                    pb[nt][i] = transpose8x8(pack2<BF16>(w0, w1));
-                }
-            // O^T += V^T P^T: rows are dims, lane (r, c) holds D / 8 of them for its four keys.
-            const uint32_t vst = st + C::kbytes + lane * C::vb;
-            if constexpr (C::k8) {
-                uint32_t w[4][C::vb / 4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (C::vb == 16) {
-                        const uint4 v = lds128(vst + i * 512);
-                        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-                    } else {
-                        const uint2 v = lds64(vst + i * 256);
-                        w[i][0] = v.x, w[i][1] = v.y;
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < C::vb / 4; ++q)
-#pragma unroll
-                    for (int hi = 0; hi < 2; ++hi) {
-                        const uint32_t pa = __byte_perm(w[0][q], w[1][q], hi ? 0x7362 : 0x5140);   // keys 2c, 2c + 1
-                        const uint32_t pc = __byte_perm(w[2][q], w[3][q], hi ? 0x7362 : 0x5140);   // keys 2c + 8, 2c + 9
-                        const uint32_t a0 = codes_to_half2<DT, 0>(pa), a1 = codes_to_half2<DT, 1>(pa);
-                        const uint32_t a2 = codes_to_half2<DT, 0>(pc), a3 = codes_to_half2<DT, 1>(pc);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                    }
-            } else {
-#pragma unroll
-                for (int e = 0; e < C::vch; ++e) {
-                    uint32_t w[4][4];
+                // O^T += V^T P^T: rows are dims, lane (r, c) holds D / 8 of them for its four keys.
+                const uint32_t vst = st + u * C::tile + C::kbytes;
+                if constexpr (C::k8) {
+                    uint32_t v[4][C::vb / 4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 v = lds128(vst + (i * C::vch + e) * 512);
-                        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+                        if constexpr (C::vb == 16) {
+                            const uint4 q4 = lds128(vst + v_read[0] + i * 512);
+                            v[i][0] = q4.x, v[i][1] = q4.y, v[i][2] = q4.z, v[i][3] = q4.w;
+                        } else {
+                            const uint2 q2 = lds64(vst + v_read[i & 1] + i * 256);
+                            v[i][0] = q2.x, v[i][1] = q2.y;
+                        }
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t a0 = __byte_perm(w[0][q], w[1][q], 0x5410), a1 = __byte_perm(w[0][q], w[1][q], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2][q], w[3][q], 0x5410), a3 = __byte_perm(w[2][q], w[3][q], 0x7632);
+                    for (int q = 0; q < C::vb / 4; ++q)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const uint32_t pa = __byte_perm(v[0][q], v[1][q], hi ? 0x7362 : 0x5140);   // keys 2c, 2c + 1
+                            const uint32_t pc = __byte_perm(v[2][q], v[3][q], hi ? 0x7362 : 0x5140);   // keys 2c + 8, 2c + 9
+                            const uint32_t a0 = codes_to_half2<DT, 0>(pa), a1 = codes_to_half2<DT, 1>(pa);
+                            const uint32_t a2 = codes_to_half2<DT, 0>(pc), a3 = codes_to_half2<DT, 1>(pc);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                        }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < C::vch; ++e) {
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 q4 = lds128(vst + v_read[0] + (i * C::vch + e) * 512);
+                            v[i][0] = q4.x, v[i][1] = q4.y, v[i][2] = q4.z, v[i][3] = q4.w;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t a0 = __byte_perm(v[0][q], v[1][q], 0x5410), a1 = __byte_perm(v[0][q], v[1][q], 0x7632);
+                            const uint32_t a2 = __byte_perm(v[2][q], v[3][q], 0x5410), a3 = __byte_perm(v[2][q], v[3][q], 0x7632);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                        }
                     }
                 }
             }
@@ -545,7 +624,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
         float* so = reinterpret_cast<float*>(smem);
         float* sm = so + kCdWarps * COLS * C::orow;
         float* sl = sm + kCdWarps * COLS;
-        float* sf = sl + kCdWarps * COLS;           // [warp][column] factor of O, then [column] M, L
+        float* sf = sl + kCdWarps * COLS;           // [warp][column] factor, then [column] M, L
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -557,7 +636,6 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 if (r == 0) {
                     sm[warp * COLS + col] = m[nt][j];
                     sl[warp * COLS + col] = sum;
-                    sf[warp * COLS + col] = R;
                 }
                 float* row = so + (warp * COLS + col) * C::orow;
 #pragma unroll
@@ -579,16 +657,13 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             for (int w = 0; w < kCdWarps; ++w) {
                 const float f = ex2_approx(sm[w * COLS + col] - M);
                 L = fmaf(sl[w * COLS + col], f, L);
-                sf[w * COLS + col] *= f;
+                sf[w * COLS + col] = f;
             }
             sM[col] = M;
             sL[col] = L;
         }
         __syncthreads();
-        const bool complete = unit0 == 0 && seg_units == sr.units;
-        // Pieces: a CTA's first segment in slot 2 cta, another in slot 2 cta + 1.
-        const int64_t piece = 2 * (int64_t)blockIdx.x + (u == u_begin ? 0 : 1);
-        float* po = p.partials + piece * COLS * (D + 2);
+        float* po = p.partials + (s_slot + index) * COLS * (D + 2);
         for (int i = threadIdx.x; i < cols * (D / 4); i += kCdThreads) {
             const int col = i / (D / 4), dim = (i % (D / 4)) * 4;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -622,53 +697,39 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 p.lse[(int64_t)b * p.HQ + hq0 + col] = L == 0.f ? -INFINITY : (M + log2f(L)) * kCdLn2;
             }
         }
-        // The next segment.
-        u += seg_units;
-        unit0 = 0;
-        if (u < u_end && ++hr == HR) {
-            hr = 0;
-            do sr = seq_range(p, ++b); while (sr.units == 0);
-        }
-        __syncthreads();        // the join is read: the ring may be filled again
     }
 }
 
 // One CTA a (sequence, query head): joins the pieces of a head whose keys several CTAs shared, in
 // key order; and writes the result of a sequence without keys.
 template <int D>
-__global__ void __launch_bounds__(kCdThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols_pow, int ctas) {
+__global__ void __launch_bounds__(kCdThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int unit) {
     constexpr int LPR = D / 4, GROUPS = kCdThreads / LPR;
-    __shared__ int64_t s_before;
+    __shared__ int64_t s_slot;
     __shared__ __align__(16) float s_o[GROUPS][D];      // written as float4
     __shared__ float s_l[GROUPS], s_m[GROUPS];
     const int b = blockIdx.x / p.HQ, hq = blockIdx.x - b * p.HQ;
-    const int CB = col_blocks(p.group, cols_pow), HR = p.c.H * CB;
-    const int h = hq / p.group, g = hq - h * p.group;
-    const int hr = h * CB + g / cols_pow, col = g % cols_pow;
-    const SeqScan scan = scan_sequences<kCdThreads>(p);
-    if (b >= scan.first && b < scan.last) {
-        int64_t before = scan.before;
-        for (int i = scan.first; i < b; ++i) before += seq_range(p, i).units;
-        s_before = before;
+    const int CB = col_blocks(p.group, cols), HR = p.c.H * CB;
+    const int h = hq / p.group, g = hq - h * p.group, cb = g / cols, col = g % cols;
+    const Cut cut = cut_sequences<kCdThreads>(p, HR, unit);
+    if (b >= cut.first && b < cut.last) {
+        int64_t slot = cut.slot;
+        for (int i = cut.first; i < b; ++i) {
+            const int n = (seq_range(p, i, unit).units + cut.chunk - 1) / cut.chunk;
+            slot += n > 1 ? (int64_t)n * HR : 0;
+        }
+        s_slot = slot;
     }
     __syncthreads();
-    const int n = seq_range(p, b).units;
-    const int64_t total = scan.total * HR, share = (total + ctas - 1) / ctas;
-    const int64_t begin = s_before * HR + (int64_t)hr * n, end = begin + n;
+    const int pieces = (seq_range(p, b, unit).units + cut.chunk - 1) / cut.chunk;
+    if (pieces == 1) return;        // its CTA wrote the result
     const int grp = threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
-    int64_t c0 = 0, c1 = -1;
-    if (n > 0) {
-        c0 = begin / share;
-        c1 = (end - 1) / share;
-        if (c0 == c1) return;   // one CTA had all its keys and wrote the result
-    }
     // Each group of lanes joins every GROUPS-th piece.
     float M = -FLT_MAX, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = c0 + grp; k <= c1; k += GROUPS) {
-        const int64_t piece = 2 * k + (max(begin, k * share) == k * share ? 0 : 1);
-        const float* po = p.partials + piece * cols_pow * (D + 2);
-        const float m = po[cols_pow * D + 2 * col], l = po[cols_pow * D + 2 * col + 1];
+    for (int k = grp; k < pieces; k += GROUPS) {
+        const float* po = p.partials + (s_slot + (int64_t)(h * pieces + k) * CB + cb) * cols * (D + 2);
+        const float m = po[cols * D + 2 * col], l = po[cols * D + 2 * col + 1];
         const float4 v = *reinterpret_cast<const float4*>(po + col * D + d);
         const float Mn = fmaxf(M, m), a = ex2_approx(M - Mn), f = ex2_approx(m - Mn);
         M = Mn;
@@ -701,24 +762,34 @@ constexpr int kMaxOcc = 4;
 int columns(int group) { return group > 8 ? 16 : 8; }
 
 template <int DT, int D, int NT>
-cudaError_t launch_split(const CacheDecodeParams& p, bool q_bf16, int nsm, cudaStream_t st) {
+cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t st) {
     using C = CdConfig<DT, D, NT>;
     static_assert(C::occ <= kMaxOcc, "the workspace counts kMaxOcc CTAs an SM");
     auto kern = cache_decode_kernel<DT, D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-    if (e != cudaSuccess) return e;
-    const int grid = nsm * C::occ;
-    kern<<<grid, kCdThreads, C::smem, st>>>(p, q_bf16);
+    cudaError_t e = cudaSuccess;
+    static std::atomic<uint64_t> ready{0};      // devices on which the kernel may have its shared memory
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const int64_t HR = (int64_t)p.c.H * col_blocks(p.group, 8 * NT);
+    p.target_chunks = kWaves * nsm * C::occ;
+    const int64_t grid = p.target_chunks + p.B * HR;     // at most so many chunks: each head rounds up once
+    if (grid > 0x7fffffffLL || (int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
+    kern<<<(unsigned)grid, kCdThreads, C::smem, st>>>(p, q_bf16);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cache_decode_merge_kernel<D><<<(unsigned)(p.B * p.HQ), kCdThreads, 0, st>>>(p, q_bf16, 8 * NT, grid);
+    cache_decode_merge_kernel<D><<<(unsigned)(p.B * p.HQ), kCdThreads, 0, st>>>(p, q_bf16, 8 * NT, C::unit);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm) {
-    return (int64_t)2 * kMaxOcc * nsm * columns(HQ / HK) * (D + 2) * 4;
+    return (int64_t)2 * kWaves * kMaxOcc * nsm * columns(HQ / HK) * (D + 2) * 4;
 }
 
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st) {

@@ -73,6 +73,7 @@ struct CacheDecodeParams {
     const float* alibi_slopes;
     int32_t score_kind;
     float* partials;
+    int32_t target_chunks;        // set by launch_cache_decode
 };
 int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm);
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st);

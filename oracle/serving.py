@@ -68,17 +68,18 @@ def quantise_e4m3(rows):
     return round_e4m3(x / scale[..., None]), np.where(bad, np.nan, scale)
 
 
-def decode(q, keys, values, length, window=0, softcap=None, slopes=None, scale=None):
+def decode(q, keys, values, length, window=0, softcap=None, slopes=None, scale=None, vscale=None):
     """q (HQ, D) over keys and values (H, n, D): (out (HQ, D), lse (HQ,), sum p |v| (HQ, D),
-    largest sum |q k| scale) with the query at position length - 1."""
+    largest sum |q k| scale, max(p s) sum |v| / s (HQ, D) with s the values' row scales (H, n) or 1)
+    with the query at position length - 1."""
     q, K, V = (np.asarray(t, dtype=np.float64) for t in (q, keys, values))
     HQ, D = q.shape
     H = K.shape[0]
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     lo = max(0, length - window) if window else 0
-    out, lse, weight, reach = np.zeros((HQ, D)), np.full(HQ, -np.inf), np.zeros((HQ, D)), 0.0
+    out, lse, weight, reach, fine = np.zeros((HQ, D)), np.full(HQ, -np.inf), np.zeros((HQ, D)), 0.0, np.zeros((HQ, D))
     if length - lo <= 0:
-        return out, lse, weight, reach
+        return out, lse, weight, reach, fine
     pos = np.arange(lo, length)
     for h in range(HQ):
         k, v = K[h // (HQ // H), lo:length], V[h // (HQ // H), lo:length]
@@ -93,4 +94,6 @@ def decode(q, keys, values, length, window=0, softcap=None, slopes=None, scale=N
         lse[h] = top + math.log(p.sum())
         p = p / p.sum()
         out[h], weight[h] = p @ v, p @ np.abs(v)
-    return out, lse, weight, reach
+        s = np.ones(len(p)) if vscale is None else np.asarray(vscale, dtype=np.float64)[h // (HQ // H), lo:length]
+        fine[h] = (p * s).max() * (np.abs(v) / s[:, None]).sum(0)
+    return out, lse, weight, reach, fine

@@ -335,17 +335,21 @@ def random_cache(kind, lens, page, H, D, seed=0, transposed=False, garbage=True,
     return cache, table, rows[0], rows[1]
 
 
-def check_decode(q, out, lse, K, V, lens, window=0, softcap=None, slopes=None, scale=None, kind="bf16"):
+def check_decode(q, out, lse, K, V, lens, window=0, softcap=None, slopes=None, scale=None, kind="bf16", vscale=None):
     # The weights are rounded to 16 bits before their product with V (bf16 for a bf16 cache,
-    # fp16 otherwise), scores are fp32 sums of D products, the result is rounded once.
+    # fp16 otherwise), scores are fp32 sums of D products, the result is rounded once.  fp16 weights
+    # (p times the value's scale, the largest at least 1) below 2^-14 are off by up to 2^-25
+    # whatever their size: 2^-25 max(p s) |v| / s of each key.
     step = HALF_STEP[torch.bfloat16 if kind == "bf16" else torch.float16]
     D = q.shape[3]
     for b, n in enumerate(lens):
-        o, l, weight, reach = ref.decode(np64(q[b, :, 0]), K[b], V[b], n, window, softcap, slopes, scale)
+        o, l, weight, reach, fine = ref.decode(np64(q[b, :, 0]), K[b], V[b], n, window, softcap, slopes, scale, vscale)
         score = D * 2.0 ** -24 * reach + 2e-6 * (1 + reach)          # a score's error
         if slopes is not None:
             score += 2.0 ** -23 * float(np.abs(slopes).max()) * max(n, 1) * 2
         tol = HALF_STEP[q.dtype] * np.abs(o) + (step + 2 * score + 1e-5) * weight + TINY[q.dtype]
+        if kind != "bf16":
+            tol += 2.0 ** -25 * fine
         got = np64(out[b, :, 0])
         assert (np.abs(got - o) <= tol).all(), (b, n, float((np.abs(got - o) / tol).max()))
         if lse is not None:
@@ -405,25 +409,51 @@ def test_decode_long_contexts_and_large_batches(kind, B, HQ, H, n):
     check_decode(q, out, lse, K, V, lens, kind=kind)
 
 
+@pytest.mark.parametrize("seed", range(6))
 @pytest.mark.parametrize("kind", ["bf16", "f16", "s8", "e4m3"])
-def test_decode_rows_of_very_different_size(kind):
+def test_decode_rows_of_very_different_size(kind, seed):
     # Scales over many orders, a key that takes all the weight late in the sequence, large and
     # tiny queries.
     fa = fa_module()
+    torch.manual_seed(seed)
     lens = [900]
-    cache, table, K, V = random_cache(kind, lens, 16, 1, 64, seed=1, garbage=False)
+    cache, table, K, V = random_cache(kind, lens, 16, 1, 64, seed=1 + seed, garbage=False)
+    vs = None
     if cache.quantised:
         f = torch.exp2(torch.randint(-20, 4, cache.v_scale.shape, device="cuda").float())
         cache.v_scale.mul_(f)
+        at = torch.arange(900, device="cuda")
+        vs = np64(cache.v_scale[table[0].long()[at // 16], :, at % 16]).T
     else:
         cache.k[table[0, 50].item(), 0, 3] *= 30
     K, V = ([gather64(cache, table, 0, 900, w)] for w in (0, 1))
-    q = rand((1, 4, 1, 64), torch.float16 if kind == "f16" else torch.bfloat16, 4)
+    q = rand((1, 4, 1, 64), torch.float16 if kind == "f16" else torch.bfloat16, 4 + seed)
     q[0, 1] *= 12
     q[0, 2] *= 2.0 ** -12 if kind == "f16" else 2.0 ** -60
     q[0, 3] = 0
     out, lse = fa.decode_attention(q, cache, table, i32(900))
-    check_decode(q, out, lse, K, V, lens, kind=kind)
+    check_decode(q, out, lse, K, V, lens, kind=kind, vscale=vs)
+
+
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+def test_decode_zero_and_tiny_value_rows(kind):
+    # Rows of zeros are stored with scale 2^-126: all of them, and a few among others.
+    fa = fa_module()
+    cache = make_cache(kind, 10, 1, 16, 64)
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    k, v = rand((1, 1, 150, 64), seed=1), torch.zeros(1, 1, 150, 64, dtype=torch.bfloat16, device="cuda")
+    q = rand((1, 2, 1, 64), seed=2, scale=2.0)
+    for live in ([], [3, 70], [149]):
+        v[:, :, live] = rand((1, 1, len(live), 64), seed=3)
+        fa.cache_append(cache, k, v, table, i32(0))
+        for tiny in (1.0, 2.0 ** -70):
+            cache.v_scale.mul_(tiny)
+            out, lse = fa.decode_attention(q, cache, table, i32(150))
+            at = torch.arange(150, device="cuda")
+            vs = np64(cache.v_scale[table[0].long()[at // 16], :, at % 16]).T
+            assert torch.isfinite(lse).all()
+            check_decode(q, out, lse, [gather64(cache, table, 0, 150, 0)], [gather64(cache, table, 0, 150, 1)], [150],
+                         kind=kind, vscale=np.maximum(vs, 2.0 ** -90))
 
 
 def gather64(cache, table, b, n, which):

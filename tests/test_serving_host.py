@@ -172,9 +172,13 @@ def test_oracle_scales():
 def test_oracle_decode_is_a_softmax():
     rng = np.random.default_rng(2)
     q, K, V = rng.standard_normal((4, 8)), rng.standard_normal((2, 9, 8)), rng.standard_normal((2, 9, 8))
-    out, lse, _, _ = ref.decode(q, K, V, 7, window=3)
+    out, lse, weight, reach, fine = ref.decode(q, K, V, 7, window=3)
     x = K[1, 4:7] @ q[3] / math.sqrt(8)
     np.testing.assert_allclose(lse[3], np.log(np.exp(x).sum()))
     np.testing.assert_allclose(out[3], np.exp(x - lse[3]) @ V[1, 4:7])
-    out, lse, _, _ = ref.decode(q, K, V, 0)
+    p = np.exp(x - lse[3])
+    np.testing.assert_allclose(weight[3], p @ np.abs(V[1, 4:7]))
+    np.testing.assert_allclose(fine[3], p.max() * np.abs(V[1, 4:7]).sum(0))
+    assert reach >= np.abs(x).max()
+    out, lse, _, _, _ = ref.decode(q, K, V, 0)
     assert not out.any() and np.isneginf(lse).all()
