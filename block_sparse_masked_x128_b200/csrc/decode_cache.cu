@@ -6,13 +6,14 @@
 //
 // The work is reading K and V once, so HBM bounds it as long as nothing else is in the way:
 //
-//   Split      the keys of every (sequence, kv head) are cut into chunks of one size, chosen on the
-//              device from the lengths so that about kWaves times as many chunks as CTAs fit on
-//              the GPU come out; one CTA takes one chunk, and the block scheduler hands them out,
-//              so ragged lengths and single long sequences load every SM alike.  A head
-//              with one chunk is finished by its CTA; otherwise the chunk's (m, l, O) goes to the
-//              workspace and the merge kernel joins the chunks in key order (no atomics: the same
-//              bits every time).
+//   Split      the keys of every (sequence, kv head) are cut into steps of 16 or 32, and the warps of
+//              one wave of CTAs take equal runs of the list of all steps, so ragged lengths and
+//              single long sequences load every SM alike.  The lengths are device data: each warp
+//              finds its run by a scan over the sequences.  A run may go through several heads; the
+//              loads run ahead across the border, so a warp's stream of copies never stops.  A head
+//              whose steps are all one warp's is finished by it; otherwise the (m, l, O) of its
+//              part goes to the workspace and the merge kernel joins the parts in key order (no
+//              atomics: the same bits every time).  Warps share nothing: no barrier anywhere.
 //   Heads      the query heads of a kv head are the columns of the products (8 or 16 at a time):
 //              S^T = K q^T and O^T = V^T P^T, with 16 keys or 16 dims as rows.  The matrix
 //              pipe is needed only because one cache byte meets up to 16 heads; at 8 columns
@@ -43,10 +44,9 @@ namespace {
 __device__ int32_t g_cache_decode_status;   // 2: a length or page out of range was met
 
 constexpr int kCdWarps = 4, kCdThreads = 32 * kCdWarps;
+constexpr int kMergeThreads = 512;
 constexpr int kTileKeys = 16;               // keys a warp takes at a time
 constexpr float kCdLn2 = 0.6931471805599453f, kCdLog2e = 1.4426950408889634f;
-constexpr int kMinChunk = 2;                // units
-constexpr int kWaves = 3;                   // chunks aimed at, in CTAs that the GPU holds at once
 constexpr float kTopWeight = 256.f;         // weights above this raise the reference
 // Value scales below 2^-90 count as 2^-90 in the reference, which bounds 2^(x - m) by 2^98: the
 // sum over 2^25 keys stays finite.
@@ -75,15 +75,10 @@ struct CdConfig {
     // overhead, where the ring has room for it.
     static constexpr int sub = D * bytes == 256 ? 1 : 2;
     static constexpr int stage = sub * tile;
-    static constexpr int occ = D * bytes == 256 ? (NT == 1 ? 3 : 2) : 3;
-    static constexpr int stages = D * bytes == 256 ? (NT == 1 ? 2 : 3) : (D * bytes == 128 ? 2 : 4);
-    static constexpr int ring = kCdWarps * stages * stage;
-    static constexpr int unit = kCdWarps * sub;           // tiles of a unit
-    // Join of the warps: O rows of D floats, 4 more after each 8 or 16 (bank conflicts).
-    static constexpr int seg = k8 && D == 128 ? 16 : 8;
-    static constexpr int orow = D + D / seg * 4;
-    static constexpr int join = 8 * NT * (kCdWarps * (orow + 3) + 2) * 4;
-    static constexpr int smem = ring > join ? ring : join;
+    static constexpr int occ = NT == 1 ? 3 : 2;
+    static constexpr int stages = (D * bytes == 64 ? 4 : 2) + (NT == 1 ? 0 : 1);
+    static constexpr int smem = kCdWarps * stages * stage;
+    static constexpr int seg = k8 && D == 128 ? 16 : 8;   // a lane's dims come in runs of this
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {
@@ -92,6 +87,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+// A kernel launched to start before its predecessor ends waits here until that has ended; the
+// predecessor lets it start once all its blocks have come to grid_dependency_release.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -147,86 +146,70 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
     return h;
 }
 
-// The keys of sequence b that are attended to, [lo, len), and their number of units.
+// The keys of sequence b that are attended to, [lo, len), from tile `tile` (of 16 keys) in `steps`
+// steps of `sub` tiles.
 struct SeqRange {
-    int32_t lo, len, tile0, tile1;       // tiles of 16 keys
-    int32_t units;
+    int32_t lo, len, tile, steps;
 };
-// `unit`: tiles of a unit.
-__device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int unit) {
+__device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int sub) {
     SeqRange r;
     const int64_t cap = min((int64_t)p.c.table_width << p.c.page_shift, (int64_t)0x7fffffc0);
     const int n = __ldg(p.kv_lens + b);
     if (n < 0 || n > cap) g_cache_decode_status = 2;
     r.len = (int32_t)max((int64_t)0, min((int64_t)n, cap));
     r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
-    r.tile0 = r.lo / kTileKeys;
-    r.tile1 = (r.len + kTileKeys - 1) / kTileKeys;
-    r.units = r.len > r.lo ? (r.tile1 - r.tile0 + unit - 1) / unit : 0;
+    r.tile = r.lo / kTileKeys;
+    r.steps = r.len > r.lo ? ((r.len + kTileKeys - 1) / kTileKeys - r.tile + sub - 1) / sub : 0;
     return r;
 }
 
-// How the sequences are cut.  Chunk i of the grid is, in order, (sequence, kv head, piece, column
-// block); a sequence has ceil(units / chunk) pieces a head.  Heads of more than one piece have
-// workspace slots, in the same order: at most 2 kWaves ctas of them, since such a head has at most
-// 2 units / chunk pieces.
-struct Cut {
-    int32_t chunk;              // units a chunk
-    int64_t before, slot;       // chunks and slots before thread t's sequences [first, last)
-    int64_t total;              // chunks of all sequences
-    int32_t first, last;
+// A warp's run of steps.  The list of steps goes by (sequence, kv head, step); `runs` warps take
+// `share` steps each.
+struct Run {
+    int32_t seq, head, step;    // where the run begins
+    int64_t first, last;        // its steps, [first, last)
+    int64_t share;
 };
-template <int THREADS>
-__device__ __forceinline__ Cut cut_sequences(const CacheDecodeParams& p, int HR, int unit) {
-    __shared__ int64_t sums[2][THREADS / 32], slots[THREADS / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = (p.B + THREADS - 1) / THREADS;
-    Cut c;
-    c.first = min(p.B, (int)threadIdx.x * n);
-    c.last = min(p.B, c.first + n);
-    int64_t units = 0;
-    for (int b = c.first; b < c.last; ++b) units += seq_range(p, b, unit).units;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) units += __shfl_xor_sync(kFullMask, units, off);
-    if (lane == 0) sums[0][warp] = units;
-    __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) all += sums[0][w];
-    all *= HR;
-    c.chunk = (int32_t)max((int64_t)kMinChunk, (all + p.target_chunks - 1) / p.target_chunks);
-    int64_t mine = 0, held = 0;
-    for (int b = c.first; b < c.last; ++b) {
-        const int pieces = (seq_range(p, b, unit).units + c.chunk - 1) / c.chunk;
-        mine += (int64_t)pieces * HR;
-        held += pieces > 1 ? (int64_t)pieces * HR : 0;
-    }
-    int64_t inc = mine, hinc = held;
+__device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int64_t which, int64_t runs) {
+    const int lane = threadIdx.x & 31;
+    const int n = (p.B + 31) / 32;
+    const int b0 = min(p.B, lane * n), b1 = min(p.B, b0 + n);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_range(p, b, sub).steps;
+    mine *= p.c.H;
+    int64_t before = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(kFullMask, inc, off), h = __shfl_up_sync(kFullMask, hinc, off);
-        if (lane >= off) {
-            inc += v;
-            hinc += h;
+        const int64_t v = __shfl_up_sync(kFullMask, before, off);
+        if (lane >= off) before += v;
+    }
+    const int64_t total = __shfl_sync(kFullMask, before, 31);
+    before -= mine;
+    Run r;
+    r.share = (total + runs - 1) / runs;
+    r.first = r.share * which;
+    r.last = min(total, r.first + r.share);
+    r.seq = -1;
+    r.head = r.step = 0;
+    if (r.first < r.last && r.first >= before && r.first < before + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const int steps = seq_range(p, b, sub).steps;
+            const int64_t k = (int64_t)steps * p.c.H;
+            if (r.first < before + k) {
+                r.seq = b;
+                r.head = (int)((r.first - before) / steps);
+                r.step = (int)((r.first - before) % steps);
+                break;
+            }
+            before += k;
         }
     }
-    if (lane == 31) {
-        sums[1][warp] = inc;
-        slots[warp] = hinc;
-    }
-    __syncthreads();
-    c.before = inc - mine;
-    c.slot = hinc - held;
-    c.total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) {
-            c.before += sums[1][w];
-            c.slot += slots[w];
-        }
-        c.total += sums[1][w];
-    }
-    return c;
+    const unsigned owner = __ballot_sync(kFullMask, r.seq >= 0);
+    const int from = owner ? __ffs(owner) - 1 : 0;
+    r.seq = __shfl_sync(kFullMask, r.seq, from);
+    r.head = __shfl_sync(kFullMask, r.head, from);
+    r.step = __shfl_sync(kFullMask, r.step, from);
+    return r;
 }
 
 // The head groups of a kv head: columns of the products, `rows` of them at a time.
@@ -240,45 +223,26 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     constexpr int KS = D / 16;                      // contraction steps of K q^T, and row tiles of O^T
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_index, s_slot;
-    __shared__ int32_t s_seq;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
 
-    // This CTA's chunk.
-    const int CB = col_blocks(p.group, COLS), HR = p.c.H * CB;
-    const Cut cut = cut_sequences<kCdThreads>(p, HR, C::unit);
-    if ((int64_t)blockIdx.x >= cut.total) return;
-    {
-        int64_t before = cut.before, slot = cut.slot;
-        for (int b = cut.first; b < cut.last; ++b) {
-            const int pieces = (seq_range(p, b, C::unit).units + cut.chunk - 1) / cut.chunk;
-            const int64_t n = (int64_t)pieces * HR;
-            if ((int64_t)blockIdx.x >= before && (int64_t)blockIdx.x < before + n) {
-                s_seq = b;
-                s_index = (int64_t)blockIdx.x - before;
-                s_slot = slot;
-            }
-            before += n;
-            slot += pieces > 1 ? n : 0;
-        }
-    }
-    __syncthreads();
-    const int b = s_seq;
-    const SeqRange sr = seq_range(p, b, C::unit);
-    const int index = (int)s_index, pieces = (sr.units + cut.chunk - 1) / cut.chunk;
-    const int cb = index % CB, piece = index / CB % pieces, h = index / CB / pieces;
-    const int col0 = cb * COLS, cols = min(COLS, p.group - col0), hq0 = h * p.group + col0;
-    const int unit0 = piece * cut.chunk, seg_units = min(cut.chunk, sr.units - unit0);
-    const bool complete = pieces == 1;
+    // With more query heads than columns, neighbouring warps take the same run for one block of
+    // columns each, so the keys are read from HBM once.
+    const int CB = col_blocks(p.group, COLS);
+    const int64_t worker = (int64_t)blockIdx.x * kCdWarps + warp;
+    const int cb = (int)(worker % CB);
+    const Run run = find_run(p, C::sub, worker / CB, (int64_t)gridDim.x * kCdWarps / CB);
+    if (run.seq < 0) return;
+    const int col0 = cb * COLS, cols = min(COLS, p.group - col0);
 
     const uint32_t ring = smem_u32(smem) + warp * C::stages * C::stage;
-    const int64_t kv_row = p.c.stride[2] * C::bytes;
+    const int64_t kv_row = p.c.stride[2] * C::bytes, page_bytes = p.c.stride[0] * C::bytes;
+    const int page_mask = (1 << p.c.page_shift) - 1;
     // Copies go by whole 128-byte lines, eight consecutive lanes a line (a 64-byte row: four), into
     // the slots of the lanes whose fragments the bytes are.  The slots' order makes the writes and
     // the reads of each quarter warp hit all banks once; with lanes of a line apart, or slots in
     // plain lane order, the copies alone ran at 5.4 TB/s instead of 7.3.
     const int krow = lane / C::lpr, kpiece = lane % C::lpr;
-    const int64_t lane_off = h * p.c.stride[1] * C::bytes + krow * kv_row + kpiece * 16;
+    const int64_t lane_off = krow * kv_row + kpiece * 16;
     const uint8_t* k_lane = static_cast<const uint8_t*>(p.c.k) + lane_off;
     const uint8_t* v_lane = static_cast<const uint8_t*>(p.c.v) + lane_off;
     // K: chunk e of rows r, r + 8 at lane (r ^ (e & 1), c)'s place.
@@ -301,12 +265,105 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     }
     const uint32_t s_slot_of_lane = (lane & 7) * 16 + (lane >> 3) * 4;     // of row r: K r, K r + 8, V r, V r + 8
     const float* s_lane = lane < 16 ? p.c.k_scale : p.c.v_scale;      // lanes 0-15 K scales, 16-31 V scales
-    if constexpr (C::k8) s_lane += h * p.c.scale_stride[1] + (lane & 15) * p.c.scale_stride[2];
-    const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
-    const int64_t page_bytes = p.c.stride[0] * C::bytes;
-    const int page_mask = (1 << p.c.page_shift) - 1;
+    if constexpr (C::k8) s_lane += (lane & 15) * p.c.scale_stride[2];
 
-    {
+    // The loads' place: the next step to bring, which may be of a later head than the one at hand.
+    struct {
+        int b, h, tile, left;           // steps left of its head
+        SeqRange sr;
+        int64_t todo;                   // steps left of the run
+        int64_t head_off, scale_off;    // the head's offset in a page
+        const int32_t* table;
+    } ld;
+    ld.b = run.seq;
+    ld.h = run.head;
+    ld.sr = seq_range(p, ld.b, C::sub);
+    ld.tile = ld.sr.tile + run.step * C::sub;
+    ld.left = ld.sr.steps - run.step;
+    ld.todo = run.last - run.first;
+    int page[C::sub];                   // looked up one step ahead of their use
+    auto look_up = [&]() {
+#pragma unroll
+        for (int u = 0; u < C::sub; ++u) {
+            const int key0 = (ld.tile + u) * kTileKeys;
+            page[u] = key0 < ld.sr.len ? __ldg(ld.table + (key0 >> p.c.page_shift)) : 0;
+        }
+    };
+    auto enter_head = [&]() {
+        ld.head_off = ld.h * p.c.stride[1] * C::bytes;
+        if constexpr (C::k8) ld.scale_off = ld.h * p.c.scale_stride[1];
+        ld.table = p.c.table + (int64_t)ld.b * p.c.table_stride;
+        look_up();
+    };
+    enter_head();
+    uint32_t bad = 0;                   // tiles of the ring whose page is out of range
+    auto issue_tile = [&](uint32_t st, int tile, int pg, uint32_t bit) {
+        const int key0 = tile * kTileKeys, row0 = key0 & page_mask;
+        const uint32_t ks = st + k_slot, vs = st + C::kbytes, ss = st + C::kbytes + C::vbytes + s_slot_of_lane;
+        const bool good = (unsigned)pg < (unsigned)p.c.n_pages;
+        const int64_t at = pg * page_bytes + row0 * kv_row + ld.head_off;
+        const uint8_t *kp = k_lane + at, *vp = v_lane + at;
+        const float* sp = s_lane;
+        if constexpr (C::k8) sp += pg * p.c.scale_stride[0] + row0 * p.c.scale_stride[2] + ld.scale_off;
+        if (good && key0 >= ld.sr.lo && key0 + kTileKeys <= ld.sr.len) {
+            bad &= ~bit;
+#pragma unroll
+            for (int j = 0; j < C::copies; ++j) cp_async16(ks + C::k_dst(j), kp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
+#pragma unroll
+            for (int j = 0; j < C::copies; ++j)
+                cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), vp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
+            if constexpr (C::k8) cp_async4(ss, sp, 4);
+        } else {
+            // Rows outside [lo, len), and a page outside the pool, are filled with zeros, not read.
+            if (!good && lane == 0) g_cache_decode_status = 2;
+            bad = good ? bad & ~bit : bad | bit;
+            auto live = [&](int row) { return good && key0 + row >= ld.sr.lo && key0 + row < ld.sr.len; };
+#pragma unroll
+            for (int j = 0; j < C::copies; ++j) {
+                const bool ok = live(krow + C::k_row(j));
+                const int64_t off = C::k_row(j) * kv_row + C::k_line(j) * 128;
+                cp_async16(ks + C::k_dst(j), ok ? kp + off : k_lane, ok ? 16 : 0);
+                cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), ok ? vp + off : v_lane, ok ? 16 : 0);
+            }
+            if constexpr (C::k8) {
+                const bool ok = live(lane & 15);
+                cp_async4(ss, ok ? sp : s_lane, ok ? 4 : 0);
+            }
+        }
+    };
+    auto issue = [&](int slot) {
+        if (ld.todo > 0) {
+#pragma unroll
+            for (int u = 0; u < C::sub; ++u)
+                issue_tile(ring + slot * C::stage + u * C::tile, ld.tile + u, page[u], 1u << (slot * C::sub + u));
+            ld.tile += C::sub;
+            if (--ld.todo > 0) {
+                if (--ld.left > 0) {
+                    look_up();
+                } else {
+                    if (++ld.h == p.c.H) {
+                        ld.h = 0;
+                        do ld.sr = seq_range(p, ++ld.b, C::sub); while (ld.sr.steps == 0);
+                    }
+                    ld.tile = ld.sr.tile;
+                    ld.left = ld.sr.steps;
+                    enter_head();
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < C::stages - 1; ++s) issue(s);
+
+    int b = run.seq, h = run.head, step0 = run.step, slot = 0;
+    SeqRange sr = seq_range(p, b, C::sub);
+    for (int64_t at = run.first; at < run.last;) {
+        // This warp's part of the head: steps step0 .. step0 + steps - 1.
+        const int steps = (int)min((int64_t)(sr.steps - step0), run.last - at);
+        const int hq0 = h * p.group + col0;
+        const bool complete = steps == sr.steps;
+
         // q as the second operand: lane (r, c) holds column r's dims of step s at
         // (16-byte chunk of 64 bytes of a K row) + 4 (step within the chunk) + 0..3.
         uint32_t qf[NT][KS][2];
@@ -372,72 +429,11 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
             for (int t = 0; t < KS; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
         }
-        // Steps of `sub` tiles: this warp's are its own of each unit.
-        const int t_end = min(sr.tile1, sr.tile0 + (unit0 + seg_units) * C::unit);
-        int t = sr.tile0 + unit0 * C::unit + warp * C::sub;   // first tile of the step at hand
-        int ti = t;                                           // first tile of the next step to load
-        uint32_t bad = 0;                                     // tiles of the ring whose page is out of range
-        // Pages are looked up one step ahead of their use.
-        int page[C::sub];
-        auto look_up = [&]() {
-#pragma unroll
-            for (int u = 0; u < C::sub; ++u)
-                page[u] = ti + u < t_end ? __ldg(table + (((ti + u) * kTileKeys) >> p.c.page_shift)) : 0;
-        };
-        look_up();
-        auto issue_tile = [&](uint32_t st, int tile, int pg, uint32_t bit) {
-            const int key0 = tile * kTileKeys, row0 = key0 & page_mask;
-            const uint32_t ks = st + k_slot, vs = st + C::kbytes, ss = st + C::kbytes + C::vbytes + s_slot_of_lane;
-            const bool good = (unsigned)pg < (unsigned)p.c.n_pages;
-            const int64_t at = pg * page_bytes + row0 * kv_row;
-            const uint8_t *kp = k_lane + at, *vp = v_lane + at;
-            const float* sp = s_lane;
-            if constexpr (C::k8) sp += pg * p.c.scale_stride[0] + row0 * p.c.scale_stride[2];
-            if (good && key0 >= sr.lo && key0 + kTileKeys <= sr.len) {
-                bad &= ~bit;
-#pragma unroll
-                for (int j = 0; j < C::copies; ++j) cp_async16(ks + C::k_dst(j), kp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
-#pragma unroll
-                for (int j = 0; j < C::copies; ++j)
-                    cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), vp + C::k_row(j) * kv_row + C::k_line(j) * 128, 16);
-                if constexpr (C::k8) cp_async4(ss, sp, 4);
-            } else {
-                // Rows outside [lo, len), and a page outside the pool, are filled with zeros, not read.
-                const bool any = tile < t_end;
-                if (any && !good && lane == 0) g_cache_decode_status = 2;
-                bad = good ? bad & ~bit : bad | bit;
-                auto live = [&](int row) { return any && good && key0 + row >= sr.lo && key0 + row < sr.len; };
-#pragma unroll
-                for (int j = 0; j < C::copies; ++j) {
-                    const bool ok = live(krow + C::k_row(j));
-                    const int64_t off = C::k_row(j) * kv_row + C::k_line(j) * 128;
-                    cp_async16(ks + C::k_dst(j), ok ? kp + off : k_lane, ok ? 16 : 0);
-                    cp_async16(vs + v_slot[C::v_odd(j)] + C::v_dst(j), ok ? vp + off : v_lane, ok ? 16 : 0);
-                }
-                if constexpr (C::k8) {
-                    const bool ok = live(lane & 15);
-                    cp_async4(ss, ok ? sp : s_lane, ok ? 4 : 0);
-                }
-            }
-        };
-        auto issue = [&](int slot) {
-#pragma unroll
-            for (int u = 0; u < C::sub; ++u)
-                issue_tile(ring + slot * C::stage + u * C::tile, ti + u, page[u], 1u << (slot * C::sub + u));
-            ti += C::unit;
-            look_up();
-        };
-#pragma unroll
-        for (int s = 0; s < C::stages - 1; ++s) {
-            if (ti < t_end) issue(s);
-            cp_async_commit();
-        }
-        int slot = 0;
-        for (; t < t_end; t += C::unit) {
+        int t = sr.tile + step0 * C::sub;       // first tile of the step at hand
+        for (int i = 0; i < steps; ++i, t += C::sub) {
             cp_async_wait<C::stages - 2>();
             __syncwarp();       // other lanes' copies have landed too; and all lanes are done with the last slot
-            if (ti < t_end) issue(slot == 0 ? C::stages - 1 : slot - 1);
-            cp_async_commit();
+            issue(slot == 0 ? C::stages - 1 : slot - 1);
             const uint32_t st = ring + slot * C::stage;
 
             // S^T: 16 keys x columns a tile; with one tile in two halves of the contraction.
@@ -617,14 +613,13 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             }
             slot = slot + 1 == C::stages ? 0 : slot + 1;
         }
-        cp_async_wait<0>();
-        __syncthreads();        // every warp is done with its ring: it now holds the join
-
-        // Join of the warps: O rows, then m, l per (warp, column), then the factors.
-        float* so = reinterpret_cast<float*>(smem);
-        float* sm = so + kCdWarps * COLS * C::orow;
-        float* sl = sm + kCdWarps * COLS;
-        float* sf = sl + kCdWarps * COLS;           // [warp][column] factor, then [column] M, L
+        // The part's (m, l, O), or the result.  A worker's first head has slot 2 worker, a later one
+        // that it leaves unfinished slot 2 worker + 1.
+        const int64_t part = 2 * worker + (at == run.first ? 0 : 1);
+        float* po = p.partials + part * COLS * (D + 2);
+        if (step0 == 0 && lane == 0)        // for the merge: the head's parts and the first one's slot
+            p.heads[((int64_t)b * p.c.H + h) * CB + cb] = make_int2(
+                complete ? 1 : (int)((at + sr.steps - 1) / run.share - worker / CB) + 1, (int)part);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -633,108 +628,91 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 float sum = l[nt][j];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
-                if (r == 0) {
-                    sm[warp * COLS + col] = m[nt][j];
-                    sl[warp * COLS + col] = sum;
-                }
-                float* row = so + (warp * COLS + col) * C::orow;
+                if (col >= cols) continue;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                uint16_t* out = p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1];
 #pragma unroll
                 for (int k = 0; k < KS; k += 2) {
-                    // dims 2k .. 2k + 3 of this lane's: contiguous within a segment of C::seg
-                    const int d = 2 * k, dim = (d / C::seg) * 64 + r * C::seg + d % C::seg;
-                    *reinterpret_cast<float4*>(row + dim + dim / C::seg * 4) = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+                    // dims 2k .. 2k + 3 of this lane's: contiguous within a run of C::seg
+                    const int dim = 2 * k / C::seg * 64 + r * C::seg + 2 * k % C::seg;
+                    const float4 v = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+                    if (!complete) {
+                        *reinterpret_cast<float4*>(po + col * D + dim) = v;
+                        continue;
+                    }
+                    uint2 w;
+                    if (q_bf16) w = make_uint2(pack2<true>(v.x * inv, v.y * inv), pack2<true>(v.z * inv, v.w * inv));
+                    else w = make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
+                    if (sum == 0.f) w = make_uint2(0, 0);
+                    *reinterpret_cast<uint2*>(out + dim) = w;
+                }
+                if (r == 0) {
+                    if (!complete) *reinterpret_cast<float2*>(po + COLS * D + 2 * col) = make_float2(m[nt][j], sum);
+                    else if (p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = sum == 0.f ? -INFINITY : (m[nt][j] + log2f(sum)) * kCdLn2;
                 }
             }
-        __syncthreads();
-        float* sM = sf + kCdWarps * COLS;
-        float* sL = sM + COLS;
-        if (threadIdx.x < COLS) {
-            const int col = threadIdx.x;
-            float M = -FLT_MAX, L = 0.f;
-#pragma unroll
-            for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, sm[w * COLS + col]);
-#pragma unroll
-            for (int w = 0; w < kCdWarps; ++w) {
-                const float f = ex2_approx(sm[w * COLS + col] - M);
-                L = fmaf(sl[w * COLS + col], f, L);
-                sf[w * COLS + col] = f;
-            }
-            sM[col] = M;
-            sL[col] = L;
-        }
-        __syncthreads();
-        float* po = p.partials + (s_slot + index) * COLS * (D + 2);
-        for (int i = threadIdx.x; i < cols * (D / 4); i += kCdThreads) {
-            const int col = i / (D / 4), dim = (i % (D / 4)) * 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kCdWarps; ++w) {
-                const float f = sf[w * COLS + col];
-                const float4 v = *reinterpret_cast<const float4*>(so + (w * COLS + col) * C::orow + dim + dim / C::seg * 4);
-                s.x = fmaf(v.x, f, s.x);
-                s.y = fmaf(v.y, f, s.y);
-                s.z = fmaf(v.z, f, s.z);
-                s.w = fmaf(v.w, f, s.w);
-            }
-            if (complete) {
-                const float L = sL[col], inv = L == 0.f ? 0.f : 1.f / L;
-                uint2 w;
-                if (q_bf16) w = make_uint2(pack2<true>(s.x * inv, s.y * inv), pack2<true>(s.z * inv, s.w * inv));
-                else w = make_uint2(pack2<false>(s.x * inv, s.y * inv), pack2<false>(s.z * inv, s.w * inv));
-                if (L == 0.f) w = make_uint2(0, 0);
-                *reinterpret_cast<uint2*>(p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1] + dim) = w;
-            } else {
-                *reinterpret_cast<float4*>(po + col * D + dim) = s;
-            }
-        }
-        if (threadIdx.x < cols) {
-            const int col = threadIdx.x;
-            const float M = sM[col], L = sL[col];
-            if (!complete) {
-                po[COLS * D + 2 * col] = M;
-                po[COLS * D + 2 * col + 1] = L;
-            } else if (p.lse) {
-                p.lse[(int64_t)b * p.HQ + hq0 + col] = L == 0.f ? -INFINITY : (M + log2f(L)) * kCdLn2;
-            }
+        // The next head.
+        at += steps;
+        step0 = 0;
+        if (at < run.last && ++h == p.c.H) {
+            h = 0;
+            do sr = seq_range(p, ++b, C::sub); while (sr.steps == 0);
         }
     }
+    cp_async_wait<0>();
+    grid_dependency_release();
 }
 
-// One CTA a (sequence, query head): joins the pieces of a head whose keys several CTAs shared, in
+// One CTA a (sequence, query head): joins the parts of a head whose keys several warps shared, in
 // key order; and writes the result of a sequence without keys.
 template <int D>
-__global__ void __launch_bounds__(kCdThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int unit) {
-    constexpr int LPR = D / 4, GROUPS = kCdThreads / LPR;
-    __shared__ int64_t s_slot;
+__global__ void __launch_bounds__(kMergeThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
+    constexpr int LPR = D / 4, GROUPS = kMergeThreads / LPR;
     __shared__ __align__(16) float s_o[GROUPS][D];      // written as float4
     __shared__ float s_l[GROUPS], s_m[GROUPS];
     const int b = blockIdx.x / p.HQ, hq = blockIdx.x - b * p.HQ;
-    const int CB = col_blocks(p.group, cols), HR = p.c.H * CB;
+    const int CB = col_blocks(p.group, cols);
     const int h = hq / p.group, g = hq - h * p.group, cb = g / cols, col = g % cols;
-    const Cut cut = cut_sequences<kCdThreads>(p, HR, unit);
-    if (b >= cut.first && b < cut.last) {
-        int64_t slot = cut.slot;
-        for (int i = cut.first; i < b; ++i) {
-            const int n = (seq_range(p, i, unit).units + cut.chunk - 1) / cut.chunk;
-            slot += n > 1 ? (int64_t)n * HR : 0;
-        }
-        s_slot = slot;
-    }
-    __syncthreads();
-    const int pieces = (seq_range(p, b, unit).units + cut.chunk - 1) / cut.chunk;
-    if (pieces == 1) return;        // its CTA wrote the result
-    const int grp = threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
-    // Each group of lanes joins every GROUPS-th piece.
+    const bool none = seq_range(p, b, sub).steps == 0;
+    grid_dependency_wait();
+    const int2 head = none ? make_int2(0, 0) : p.heads[((int64_t)b * p.c.H + h) * CB + cb];
+    const int pieces = head.x;
+    if (pieces == 1) return;        // its warp wrote the result
+    // Each group of lanes joins every groups-th part, kAhead of them loaded at a time: the parts are
+    // in L2, so their latency is the cost.  The first is in slot head.y, the others are the first
+    // of the following workers of this block of columns.
+    constexpr int kAhead = 4;
+    const int groups = blockDim.x / LPR, grp = threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
+    const int64_t step = (int64_t)2 * CB;
     float M = -FLT_MAX, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = grp; k < pieces; k += GROUPS) {
-        const float* po = p.partials + (s_slot + (int64_t)(h * pieces + k) * CB + cb) * cols * (D + 2);
-        const float m = po[cols * D + 2 * col], l = po[cols * D + 2 * col + 1];
-        const float4 v = *reinterpret_cast<const float4*>(po + col * D + d);
-        const float Mn = fmaxf(M, m), a = ex2_approx(M - Mn), f = ex2_approx(m - Mn);
+    for (int k0 = grp; k0 < pieces; k0 += groups * kAhead) {
+        float2 ml[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i * groups;
+            ml[i] = make_float2(-FLT_MAX, 0.f);
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < pieces) {
+                const float* po = p.partials + (k == 0 ? (int64_t)head.y : (head.y & ~1) + k * step) * cols * (D + 2);
+                ml[i] = *reinterpret_cast<const float2*>(po + cols * D + 2 * col);
+                v[i] = *reinterpret_cast<const float4*>(po + col * D + d);
+            }
+        }
+        float Mn = M;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) Mn = fmaxf(Mn, ml[i].x);
+        const float a = ex2_approx(M - Mn);
         M = Mn;
-        L = L * a + l * f;
-        O = make_float4(O.x * a + v.x * f, O.y * a + v.y * f, O.z * a + v.z * f, O.w * a + v.w * f);
+        L *= a;
+        O = make_float4(O.x * a, O.y * a, O.z * a, O.w * a);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float f = ex2_approx(ml[i].x - M);
+            L = fmaf(ml[i].y, f, L);
+            O = make_float4(fmaf(v[i].x, f, O.x), fmaf(v[i].y, f, O.y), fmaf(v[i].z, f, O.z), fmaf(v[i].w, f, O.w));
+        }
     }
     *reinterpret_cast<float4*>(&s_o[grp][d]) = O;
     if (d == 0) {
@@ -743,14 +721,11 @@ __global__ void __launch_bounds__(kCdThreads) cache_decode_merge_kernel(const __
     }
     __syncthreads();
     float MM = -FLT_MAX, LL = 0.f;
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) MM = fmaxf(MM, s_m[i]);
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) LL = fmaf(s_l[i], ex2_approx(s_m[i] - MM), LL);
+    for (int i = 0; i < groups; ++i) MM = fmaxf(MM, s_m[i]);
+    for (int i = 0; i < groups; ++i) LL = fmaf(s_l[i], ex2_approx(s_m[i] - MM), LL);
     if (threadIdx.x < D) {
         float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) v = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - MM), v);
+        for (int i = 0; i < groups; ++i) v = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - MM), v);
         v = LL == 0.f ? 0.f : v / LL;
         p.out[b * p.out_stride[0] + (int64_t)hq * p.out_stride[1] + threadIdx.x] =
             (uint16_t)((q_bf16 ? pack2<true>(v, 0.f) : pack2<false>(v, 0.f)) & 0xFFFFu);
@@ -758,8 +733,14 @@ __global__ void __launch_bounds__(kCdThreads) cache_decode_merge_kernel(const __
     if (threadIdx.x == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq] = LL == 0.f ? -INFINITY : (MM + log2f(LL)) * kCdLn2;
 }
 
-constexpr int kMaxOcc = 4;
+constexpr int kMaxOcc = 3;
 int columns(int group) { return group > 8 ? 16 : 8; }
+
+// The workspace: the table of heads, then the slots.
+int64_t heads_bytes(int64_t B, int64_t HQ, int64_t HK) {
+    const int group = (int)(HQ / HK);
+    return (B * HK * col_blocks(group, columns(group)) * 8 + 15) / 16 * 16;
+}
 
 template <int DT, int D, int NT>
 cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t st) {
@@ -775,21 +756,31 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    const int64_t HR = (int64_t)p.c.H * col_blocks(p.group, 8 * NT);
-    p.target_chunks = kWaves * nsm * C::occ;
-    const int64_t grid = p.target_chunks + p.B * HR;     // at most so many chunks: each head rounds up once
-    if (grid > 0x7fffffffLL || (int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<(unsigned)grid, kCdThreads, C::smem, st>>>(p, q_bf16);
+    p.heads = static_cast<int2*>(p.workspace);
+    p.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + heads_bytes(p.B, p.HQ, p.c.H));
+    const int grid = nsm * C::occ;
+    if ((int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
+    kern<<<grid, kCdThreads, C::smem, st>>>(p, q_bf16);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cache_decode_merge_kernel<D><<<(unsigned)(p.B * p.HQ), kCdThreads, 0, st>>>(p, q_bf16, 8 * NT, C::unit);
-    return cudaGetLastError();
+    // The merge may start while the last chunks run: it has the cut to work out first.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.B * p.HQ));
+    // Few heads may have many parts each; many heads have few.
+    cfg.blockDim = dim3((int64_t)p.B * p.HQ <= 2 * nsm ? kMergeThreads : 128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_decode_merge_kernel<D>, (const CacheDecodeParams&)p, q_bf16, 8 * NT, (int)C::sub);
 }
 
 }  // namespace
 
 int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm) {
-    return (int64_t)2 * kWaves * kMaxOcc * nsm * columns(HQ / HK) * (D + 2) * 4;
+    return heads_bytes(B, HQ, HK) + (int64_t)2 * kMaxOcc * kCdWarps * nsm * columns(HQ / HK) * (D + 2) * 4;
 }
 
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st) {

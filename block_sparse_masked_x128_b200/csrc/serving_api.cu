@@ -365,7 +365,7 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     p.softcap_k = (float)(2.0 / cap);
     p.alibi_slopes = params ? params->alibi_slopes : nullptr;
     p.score_kind = (int32_t)score_mod_kind;
-    p.partials = static_cast<float*>(workspace);
+    p.workspace = workspace;
     const cudaError_t e = fa::launch_cache_decode(p, cache->dtype, (int)q->D, q->dtype == FA_DTYPE_BF16, nsm,
                                                   static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? fa::record_ok() : cuda_fail(e, "decode launch");
