@@ -87,10 +87,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// A kernel launched to start before its predecessor ends waits here until that has ended; the
-// predecessor lets it start once all its blocks have come to grid_dependency_release.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dependency_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -153,14 +149,18 @@ struct SeqRange {
 };
 __device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int sub) {
     SeqRange r;
-    const int64_t cap = min((int64_t)p.c.table_width << p.c.page_shift, (int64_t)0x7fffffc0);
     const int n = __ldg(p.kv_lens + b);
-    if (n < 0 || n > cap) g_cache_decode_status = 2;
-    r.len = (int32_t)max((int64_t)0, min((int64_t)n, cap));
+    if ((unsigned)n > (unsigned)p.capacity) g_cache_decode_status = 2;
+    r.len = max(0, min(n, p.capacity));
     r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
     r.tile = r.lo / kTileKeys;
     r.steps = r.len > r.lo ? ((r.len + kTileKeys - 1) / kTileKeys - r.tile + sub - 1) / sub : 0;
     return r;
+}
+
+// Division of counts of steps: 32 bits wherever they fit, which they do unless terabytes are read.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // A warp's run of steps.  The list of steps goes by (sequence, kv head, step); `runs` warps take
@@ -186,7 +186,7 @@ __device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int
     const int64_t total = __shfl_sync(kFullMask, before, 31);
     before -= mine;
     Run r;
-    r.share = (total + runs - 1) / runs;
+    r.share = divide(total + runs - 1, runs);
     r.first = r.share * which;
     r.last = min(total, r.first + r.share);
     r.seq = -1;
@@ -197,8 +197,8 @@ __device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int
             const int64_t k = (int64_t)steps * p.c.H;
             if (r.first < before + k) {
                 r.seq = b;
-                r.head = (int)((r.first - before) / steps);
-                r.step = (int)((r.first - before) % steps);
+                r.head = (int)divide(r.first - before, steps);
+                r.step = (int)(r.first - before - (int64_t)r.head * steps);
                 break;
             }
             before += k;
@@ -225,12 +225,13 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
 
+    grid_dependency_wait();
     // With more query heads than columns, neighbouring warps take the same run for one block of
     // columns each, so the keys are read from HBM once.
     const int CB = col_blocks(p.group, COLS);
-    const int64_t worker = (int64_t)blockIdx.x * kCdWarps + warp;
-    const int cb = (int)(worker % CB);
-    const Run run = find_run(p, C::sub, worker / CB, (int64_t)gridDim.x * kCdWarps / CB);
+    const int worker = blockIdx.x * kCdWarps + warp;
+    const int mine = worker / CB, cb = worker - mine * CB;
+    const Run run = find_run(p, C::sub, mine, (int)(gridDim.x * kCdWarps) / CB);
     if (run.seq < 0) return;
     const int col0 = cb * COLS, cols = min(COLS, p.group - col0);
 
@@ -615,11 +616,11 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
         }
         // The part's (m, l, O), or the result.  A worker's first head has slot 2 worker, a later one
         // that it leaves unfinished slot 2 worker + 1.
-        const int64_t part = 2 * worker + (at == run.first ? 0 : 1);
-        float* po = p.partials + part * COLS * (D + 2);
+        const int part = 2 * worker + (at == run.first ? 0 : 1);
+        float* po = p.partials + (int64_t)part * COLS * (D + 2);
         if (step0 == 0 && lane == 0)        // for the merge: the head's parts and the first one's slot
             p.heads[((int64_t)b * p.c.H + h) * CB + cb] = make_int2(
-                complete ? 1 : (int)((at + sr.steps - 1) / run.share - worker / CB) + 1, (int)part);
+                complete ? 1 : (int)divide(at + sr.steps - 1, run.share) - mine + 1, part);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -629,26 +630,24 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
                 if (col >= cols) continue;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                uint16_t* out = p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1];
+                // dims 2k .. 2k + 3 of this lane's: contiguous within a run of C::seg
+                auto dim = [&](int k) { return 2 * k / C::seg * 64 + r * C::seg + 2 * k % C::seg; };
+                if (!complete) {
 #pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    // dims 2k .. 2k + 3 of this lane's: contiguous within a run of C::seg
-                    const int dim = 2 * k / C::seg * 64 + r * C::seg + 2 * k % C::seg;
-                    const float4 v = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
-                    if (!complete) {
-                        *reinterpret_cast<float4*>(po + col * D + dim) = v;
-                        continue;
+                    for (int k = 0; k < KS; k += 2)
+                        *reinterpret_cast<float4*>(po + col * D + dim(k)) = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+                    if (r == 0) *reinterpret_cast<float2*>(po + COLS * D + 2 * col) = make_float2(m[nt][j], sum);
+                } else {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    uint16_t* out = p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1];
+#pragma unroll
+                    for (int k = 0; k < KS; k += 2) {
+                        const float4 v = make_float4(o[nt][k][j] * inv, o[nt][k][2 + j] * inv, o[nt][k + 1][j] * inv, o[nt][k + 1][2 + j] * inv);
+                        uint2 w = q_bf16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w)) : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+                        if (sum == 0.f) w = make_uint2(0, 0);
+                        *reinterpret_cast<uint2*>(out + dim(k)) = w;
                     }
-                    uint2 w;
-                    if (q_bf16) w = make_uint2(pack2<true>(v.x * inv, v.y * inv), pack2<true>(v.z * inv, v.w * inv));
-                    else w = make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
-                    if (sum == 0.f) w = make_uint2(0, 0);
-                    *reinterpret_cast<uint2*>(out + dim) = w;
-                }
-                if (r == 0) {
-                    if (!complete) *reinterpret_cast<float2*>(po + COLS * D + 2 * col) = make_float2(m[nt][j], sum);
-                    else if (p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = sum == 0.f ? -INFINITY : (m[nt][j] + log2f(sum)) * kCdLn2;
+                    if (r == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = sum == 0.f ? -INFINITY : (m[nt][j] + log2f(sum)) * kCdLn2;
                 }
             }
         // The next head.
@@ -665,16 +664,16 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 
 // One CTA a (sequence, query head): joins the parts of a head whose keys several warps shared, in
 // key order; and writes the result of a sequence without keys.
-template <int D>
+template <int D, int SLICES>
 __global__ void __launch_bounds__(kMergeThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
-    constexpr int LPR = D / 4, GROUPS = kMergeThreads / LPR;
-    __shared__ __align__(16) float s_o[GROUPS][D];      // written as float4
-    __shared__ float s_l[GROUPS], s_m[GROUPS];
+    constexpr int DS = D / SLICES, LPR = DS / 4, WARPS = kMergeThreads / 32;     // dims of this CTA
+    __shared__ __align__(16) float s_o[WARPS][DS];      // written as float4
+    __shared__ float s_l[WARPS], s_m[WARPS];
     const int b = blockIdx.x / p.HQ, hq = blockIdx.x - b * p.HQ;
     const int CB = col_blocks(p.group, cols);
     const int h = hq / p.group, g = hq - h * p.group, cb = g / cols, col = g % cols;
-    const bool none = seq_range(p, b, sub).steps == 0;
     grid_dependency_wait();
+    const bool none = seq_range(p, b, sub).steps == 0;
     const int2 head = none ? make_int2(0, 0) : p.heads[((int64_t)b * p.c.H + h) * CB + cb];
     const int pieces = head.x;
     if (pieces == 1) return;        // its warp wrote the result
@@ -697,7 +696,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_decode_merge_kernel(const
             if (k < pieces) {
                 const float* po = p.partials + (k == 0 ? (int64_t)head.y : (head.y & ~1) + k * step) * cols * (D + 2);
                 ml[i] = *reinterpret_cast<const float2*>(po + cols * D + 2 * col);
-                v[i] = *reinterpret_cast<const float4*>(po + col * D + d);
+                v[i] = *reinterpret_cast<const float4*>(po + col * D + blockIdx.y * DS + d);
             }
         }
         float Mn = M;
@@ -714,23 +713,36 @@ __global__ void __launch_bounds__(kMergeThreads) cache_decode_merge_kernel(const
             O = make_float4(fmaf(v[i].x, f, O.x), fmaf(v[i].y, f, O.y), fmaf(v[i].z, f, O.z), fmaf(v[i].w, f, O.w));
         }
     }
-    *reinterpret_cast<float4*>(&s_o[grp][d]) = O;
-    if (d == 0) {
-        s_m[grp] = M;
-        s_l[grp] = L;
+    // The groups of a warp, then the warps.
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) {
+        const float Mo = __shfl_xor_sync(kFullMask, M, off), Lo = __shfl_xor_sync(kFullMask, L, off);
+        const float Mn = fmaxf(M, Mo), fa = ex2_approx(M - Mn), fb = ex2_approx(Mo - Mn);
+        M = Mn;
+        L = L * fa + Lo * fb;
+        O.x = O.x * fa + __shfl_xor_sync(kFullMask, O.x, off) * fb;
+        O.y = O.y * fa + __shfl_xor_sync(kFullMask, O.y, off) * fb;
+        O.z = O.z * fa + __shfl_xor_sync(kFullMask, O.z, off) * fb;
+        O.w = O.w * fa + __shfl_xor_sync(kFullMask, O.w, off) * fb;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (lane < LPR) *reinterpret_cast<float4*>(&s_o[warp][d]) = O;
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
     }
     __syncthreads();
     float MM = -FLT_MAX, LL = 0.f;
-    for (int i = 0; i < groups; ++i) MM = fmaxf(MM, s_m[i]);
-    for (int i = 0; i < groups; ++i) LL = fmaf(s_l[i], ex2_approx(s_m[i] - MM), LL);
-    if (threadIdx.x < D) {
+    for (int i = 0; i < warps; ++i) MM = fmaxf(MM, s_m[i]);
+    for (int i = 0; i < warps; ++i) LL = fmaf(s_l[i], ex2_approx(s_m[i] - MM), LL);
+    if (threadIdx.x < DS) {
         float v = 0.f;
-        for (int i = 0; i < groups; ++i) v = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - MM), v);
+        for (int i = 0; i < warps; ++i) v = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - MM), v);
         v = LL == 0.f ? 0.f : v / LL;
-        p.out[b * p.out_stride[0] + (int64_t)hq * p.out_stride[1] + threadIdx.x] =
+        p.out[b * p.out_stride[0] + (int64_t)hq * p.out_stride[1] + blockIdx.y * DS + threadIdx.x] =
             (uint16_t)((q_bf16 ? pack2<true>(v, 0.f) : pack2<false>(v, 0.f)) & 0xFFFFu);
     }
-    if (threadIdx.x == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq] = LL == 0.f ? -INFINITY : (MM + log2f(LL)) * kCdLn2;
+    if (threadIdx.x == 0 && blockIdx.y == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq] = LL == 0.f ? -INFINITY : (MM + log2f(LL)) * kCdLn2;
 }
 
 constexpr int kMaxOcc = 3;
@@ -760,21 +772,13 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     p.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + heads_bytes(p.B, p.HQ, p.c.H));
     const int grid = nsm * C::occ;
     if ((int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<grid, kCdThreads, C::smem, st>>>(p, q_bf16);
-    e = cudaGetLastError();
+    e = launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p, q_bf16);
     if (e != cudaSuccess) return e;
-    // The merge may start while the last chunks run: it has the cut to work out first.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.B * p.HQ));
-    // Few heads may have many parts each; many heads have few.
-    cfg.blockDim = dim3((int64_t)p.B * p.HQ <= 2 * nsm ? kMergeThreads : 128);
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_decode_merge_kernel<D>, (const CacheDecodeParams&)p, q_bf16, 8 * NT, (int)C::sub);
+    // The merge: few heads may have many parts each (four CTAs a head), many heads have few.
+    const int64_t heads = (int64_t)p.B * p.HQ;
+    const int cols = 8 * NT, sub = C::sub;
+    if (heads <= nsm) return launch_early(cache_decode_merge_kernel<D, 4>, dim3((unsigned)heads, 4), dim3(kMergeThreads), 0, st, p, q_bf16, cols, sub);
+    return launch_early(cache_decode_merge_kernel<D, 1>, dim3((unsigned)heads), dim3(128), 0, st, p, q_bf16, cols, sub);
 }
 
 }  // namespace

@@ -69,6 +69,7 @@ struct CacheDecodeParams {
     int32_t B, HQ, group;         // group = query heads a kv head
     const int32_t* kv_lens;       // [B]
     int32_t window;               // 0: all keys
+    int32_t capacity;             // tokens that a page table row maps
     float scale_log2, softcap_log2, softcap_k;   // softcap_k: 2 / softcap
     const float* alibi_slopes;
     int32_t score_kind;
@@ -82,6 +83,29 @@ cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bo
 cudaError_t cache_decode_status(cudaStream_t st, int32_t* out);
 
 #ifdef __CUDACC__
+// The kernels of these operators are short and follow one another: each is launched so that it may
+// start before its predecessor on the stream ends, and its first act is to wait for that end
+// (with all the predecessor's writes) before it reads or writes anything.  What overlaps is the
+// launch.  A kernel that comes to grid_dependency_release in all its blocks lets its successor
+// start there rather than at its own end.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The page of block `blk` of sequence b, or -1 where the table has none or an index outside
 // the pool.
 __device__ __forceinline__ int cache_page(const CacheView& c, int b, int64_t blk) {

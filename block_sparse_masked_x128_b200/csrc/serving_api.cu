@@ -360,6 +360,9 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     p.group = (int32_t)(q->H / cache->H);
     p.kv_lens = kv_lens;
     p.window = window;
+    // The kernels count keys in 32 bits (2^31 - 64 tokens a sequence at most).
+    const int64_t capacity = table_width << p.c.page_shift;
+    p.capacity = (int32_t)(capacity < 0x7fffffc0 ? capacity : 0x7fffffc0);
     p.scale_log2 = (float)(sc * log2e);
     p.softcap_log2 = (float)(cap * log2e);
     p.softcap_k = (float)(2.0 / cap);
