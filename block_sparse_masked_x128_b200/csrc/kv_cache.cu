@@ -24,6 +24,7 @@ namespace {
 __device__ int32_t g_cache_rows_status;   // 2: a page or position out of range was met
 
 constexpr int kRowThreads = 128;
+constexpr int kRowsAhead = 2;         // rows of k and of v a lane group has in flight
 
 template <bool BF16>
 __device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
@@ -78,59 +79,78 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-// Grid (ceil(S / rows), H, B).
+// The code bytes of a row's eight values and its scale; `amax` holds the bits of its largest
+// magnitude.
+template <int DT>
+__device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t amax, float& scale) {
+    scale = row_scale<DT>(amax);
+    uint32_t c[2] = {0u, 0u};
+    if (amax < 0x7f800000u) {
+        const float inv = __frcp_rn(scale);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t two;
+            if constexpr (DT == FA_DTYPE_S8)
+                two = (uint32_t)(quantise_s8(x[2 * i], scale, inv) & 0xFF) | (uint32_t)(quantise_s8(x[2 * i + 1], scale, inv) & 0xFF) << 8;
+            else
+                two = quantise_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+            c[i / 2] |= two << (16 * (i % 2));
+        }
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+// Grid (ceil(S / (groups kRowsAhead)), H, B): a group of D / 8 lanes takes kRowsAhead rows, all
+// loaded before the first is worked on.
 template <int DT, int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheRowsParams p) {
     constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
-    const int s = blockIdx.x * RPC + threadIdx.x / LPR;
+    const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
     const int count = p.limit ? min(__ldg(p.limit + b), p.S) : p.S;
-    int page = -1;
-    int64_t pos = 0;
-    if (s < count) {
-        pos = (p.start ? (int64_t)__ldg(p.start + b) : 0) + s;
-        page = pos < 0 ? -1 : cache_page(p.c, b, pos >> p.c.page_shift);
-        if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+    const int64_t start = __ldg(p.start + b);
+    uint4 raw[kRowsAhead][2];
+    int page[kRowsAhead];
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+        const int s = s0 + i * RPC;
+        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+        page[i] = -1;
+        if (s < count) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                raw[i][w] = *reinterpret_cast<const uint4*>(p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8);
+            const int64_t pos = start + s;
+            page[i] = pos < 0 ? -1 : cache_page(p.c, b, pos >> p.c.page_shift);
+            if (page[i] < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+        }
     }
-    const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (page >= 0)
-            r = *reinterpret_cast<const uint4*>(p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8);
-        const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
-        void* pool = w ? p.c.v : p.c.k;
-        if constexpr (!CacheType<DT>::k8) {
-            if (page >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) = r;
-        } else {
-            float x[8];
-            row_unpack<BF16>(r, x);
-            uint32_t m = 0;
+    for (int i = 0; i < kRowsAhead; ++i) {
+        const int row = (int)((start + s0 + i * RPC) & ((1 << p.c.page_shift) - 1));
+        const int64_t at = (int64_t)page[i] * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+        const int64_t sat = (int64_t)page[i] * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        for (int w = 0; w < 2; ++w) {
+            void* pool = w ? p.c.v : p.c.k;
+            if constexpr (!CacheType<DT>::k8) {
+                if (page[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) = raw[i][w];
+            } else {
+                float x[8];
+                row_unpack<BF16>(raw[i][w], x);
+                uint32_t m = 0;
 #pragma unroll
-            for (int off = LPR / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
-            const float scale = row_scale<DT>(m);
-            uint32_t c[2] = {0u, 0u};
-            if (m < 0x7f800000u) {
-                const float inv = __frcp_rn(scale);
+                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t two;
-                    if constexpr (DT == FA_DTYPE_S8)
-                        two = (uint32_t)(quantise_s8(x[2 * i], scale, inv) & 0xFF) |
-                              (uint32_t)(quantise_s8(x[2 * i + 1], scale, inv) & 0xFF) << 8;
-                    else
-                        two = quantise_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-                    c[i / 2] |= two << (16 * (i % 2));
+                for (int off = LPR / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+                float scale;
+                const uint2 c = quantise_row<DT>(x, m, scale);
+                if (page[i] >= 0) {
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = c;
+                    if (sub == 0) (w ? p.c.v_scale : p.c.k_scale)[sat] = scale;
                 }
-            }
-            if (page >= 0) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = make_uint2(c[0], c[1]);
-                if (sub == 0)
-                    (w ? p.c.v_scale : p.c.k_scale)[(int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] +
-                                                    (int64_t)row * p.c.scale_stride[2]] = scale;
             }
         }
     }
@@ -140,53 +160,72 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
 template <int DT, int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
     constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
-    const int s = blockIdx.x * RPC + threadIdx.x / LPR;
+    const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
-    if (s >= p.S) return;
-    const int64_t pos = (p.start ? (int64_t)__ldg(p.start + b) : 0) + s;
-    int page = -1;
-    if (pos >= 0 && pos < __ldg(p.limit + b)) {
-        page = cache_page(p.c, b, pos >> p.c.page_shift);
-        if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
-    }
-    const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
+    const int64_t start = p.start ? (int64_t)__ldg(p.start + b) : 0;
+    const int len = __ldg(p.limit + b);
+    uint4 raw[kRowsAhead][2];
+    float scale[kRowsAhead][2];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-            const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+    for (int i = 0; i < kRowsAhead; ++i) {
+        const int64_t pos = start + s0 + i * RPC;
+        int page = -1;
+        if (s0 + i * RPC < p.S && pos >= 0 && pos < len) {
+            page = cache_page(p.c, b, pos >> p.c.page_shift);
+            if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+        }
+        const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
+        const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+        const int64_t sat = (int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            raw[i][w] = make_uint4(0, 0, 0, 0);
+            scale[i][w] = 0.f;
+            if (page < 0) continue;
             const void* pool = w ? p.c.v : p.c.k;
             if constexpr (!CacheType<DT>::k8) {
-                r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pool) + at);
+                raw[i][w] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pool) + at);
             } else {
                 const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + at);
-                const float scale = (w ? p.c.v_scale : p.c.k_scale)[(int64_t)page * p.c.scale_stride[0] +
-                                                                    h * p.c.scale_stride[1] +
-                                                                    (int64_t)row * p.c.scale_stride[2]];
+                raw[i][w].x = c.x;
+                raw[i][w].y = c.y;
+                scale[i][w] = (w ? p.c.v_scale : p.c.k_scale)[sat];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsAhead; ++i) {
+        const int s = s0 + i * RPC;
+        if (s >= p.S) continue;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint4 r = raw[i][w];
+            if constexpr (CacheType<DT>::k8) {
                 uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = ((i < 2 ? c.x : c.y) >> (16 * (i % 2))) & 0xFFFFu;
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t two = ((e < 2 ? raw[i][w].x : raw[i][w].y) >> (16 * (e % 2))) & 0xFFFFu;
                     float2 f;
                     if constexpr (DT == FA_DTYPE_S8) f = make_float2((float)(int8_t)(two & 0xFF), (float)(int8_t)(two >> 8));
                     else f = value_e4m3x2(two);
-                    o[i] = pack2<BF16>(f.x * scale, f.y * scale);
+                    o[e] = pack2<BF16>(f.x * scale[i][w], f.y * scale[i][w]);
                 }
                 r = make_uint4(o[0], o[1], o[2], o[3]);
             }
+            *reinterpret_cast<uint4*>(p.out[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8) = r;
         }
-        *reinterpret_cast<uint4*>(p.out[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8) = r;
     }
 }
 
 template <int DT, int D, bool BF16>
 cudaError_t launch_rows(const CacheRowsParams& p, bool append, cudaStream_t st) {
     constexpr int RPC = kRowThreads / (D / 8);
-    const dim3 grid((unsigned)((p.S + RPC - 1) / RPC), (unsigned)p.c.H, (unsigned)p.B);
-    if (append) cache_append_kernel<DT, D, BF16><<<grid, kRowThreads, 0, st>>>(p);
-    else cache_read_kernel<DT, D, BF16><<<grid, kRowThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    constexpr int rows = RPC * kRowsAhead;
+    const dim3 grid((unsigned)((p.S + rows - 1) / rows), (unsigned)p.c.H, (unsigned)p.B), block(kRowThreads);
+    return append ? launch_early(cache_append_kernel<DT, D, BF16>, grid, block, 0, st, p)
+                  : launch_early(cache_read_kernel<DT, D, BF16>, grid, block, 0, st, p);
 }
 
 cudaError_t launch_any(const CacheRowsParams& p, int dtype, int D, bool bf16, bool append, cudaStream_t st) {
