@@ -56,91 +56,110 @@ __device__ __forceinline__ void rot_unpack8(const uint4& r, float (&f)[8]) {
     }
 }
 
-// A token's offset in the inputs and outputs, and the row of one of its heads (q's, then k's).
-struct RotToken {
-    int64_t x[2], y[2];
-};
-struct RotRow {
-    const uint16_t* x;
-    uint16_t* y;
-};
-__device__ __forceinline__ RotToken rot_token(const RotaryParams& p, int64_t tok) {
-    const int b = (int)tok / p.S, s = (int)tok - b * p.S;       // fewer than 2^31 tokens
-    return {{b * p.xs[0][0] + s * p.xs[0][2], b * p.xs[1][0] + s * p.xs[1][2]},
-            {b * p.ys[0][0] + s * p.ys[0][2], b * p.ys[1][0] + s * p.ys[1][2]}};
-}
-__device__ __forceinline__ RotRow rot_row(const RotaryParams& p, const RotToken& t, int head) {
-    if (head < p.H[0]) return {p.x[0] + t.x[0] + head * p.xs[0][1], p.y[0] + t.y[0] + head * p.ys[0][1]};
-    const int h = head - p.H[0];
-    return {p.x[1] + t.x[1] + h * p.xs[1][1], p.y[1] + t.y[1] + h * p.ys[1][1]};
+// cos and sin (times the factor) of the first `half` pairs of tokens t0 .. t0 + nt - 1 of sequence
+// b, pair j of token t at cs[t * pitch + place(j)].
+template <class Place>
+__device__ __forceinline__ void rot_table(const RotaryParams& p, float2* cs, int b, int t0, int nt, int pitch, Place&& place) {
+    for (int i = threadIdx.x; i < nt * p.half; i += kRotThreads) {
+        const int t = i / p.half, j = i - t * p.half, s = t0 + t;
+        const int64_t pos = p.pos ? (int64_t)__ldg(p.pos + b * p.pos_stride + s * p.pos_token_stride) : p.pos0 + s * p.pos_token_stride;
+        cs[t * pitch + place(j)] = rotary_cos_sin(__ldg(p.freq + j), pos, p.factor, p.inverse != 0);
+    }
 }
 
-// cos and sin (times the factor) of pairs pair0 .. pair0 + np - 1 of tokens t0 .. t0 + nt - 1.
-__device__ __forceinline__ void rot_table(const RotaryParams& p, float2* cs, int64_t t0, int nt, int pair0, int np) {
-    for (int i = threadIdx.x; i < nt * np; i += kRotThreads) {
-        const int t = i / np, j = i - t * np;
-        const int tok = (int)(t0 + t), b = tok / p.S, s = tok - b * p.S;
-        const int64_t pos = p.pos ? (int64_t)__ldg(p.pos + b * p.pos_stride + s) : p.pos0 + s;
-        cs[i] = rotary_cos_sin(__ldg(p.freq + pair0 + j), pos, p.factor, p.inverse != 0);
-    }
+// A CTA's tokens, of one sequence, and its heads, of all those of q and k.
+struct RotTile {
+    int b, t0, nt, h0, h1;
+};
+__device__ __forceinline__ RotTile rot_tile(const RotaryParams& p) {
+    RotTile r;
+    r.b = blockIdx.x / p.ctas_per_seq;
+    r.t0 = (blockIdx.x - r.b * p.ctas_per_seq) * p.tokens_per_cta;
+    r.nt = min(p.tokens_per_cta, p.S - r.t0);
+    const int heads = p.H[0] + p.H[1];
+    r.h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y);
+    r.h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
+    return r;
 }
 
 // By columns: half layout with rot_dim a multiple of 16, or interleaved with any rot_dim.
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kRotThreads) rotary_columns_kernel(const __grid_constant__ RotaryParams p) {
-    __shared__ float2 cs[kRotTable];
+__global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __grid_constant__ RotaryParams p) {
+    __shared__ __align__(16) float2 cs[kRotTable];
     constexpr int kAhead = INTER ? 4 : 2;          // rows whose 16-byte loads are in flight at once
+    constexpr int J = INTER ? 4 : 8;               // pairs a column
     grid_dependency_wait();
-    const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
-    const int nt = (int)min((int64_t)p.tokens_per_cta, (int64_t)p.B * p.S - t0);
-    const int heads = p.H[0] + p.H[1];
-    const int h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y), h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
+    const RotTile tile = rot_tile(p);
     // The columns of a row: rotated ones (half layout: pairs of columns), then copied ones.
-    const int rot_cols = INTER ? (p.half + 3) / 4 : p.half / 8;
+    const int rot_cols = (p.half + J - 1) / J;
     const int copied0 = INTER ? rot_cols * 8 : 2 * p.half;
     const int cols = rot_cols + (p.in_place ? 0 : (p.D - copied0) / 8);
     const int col = threadIdx.x % cols, first = threadIdx.x / cols, stride = kRotThreads / cols;   // D <= 1024: cols <= 128
-    rot_table(p, cs, t0, nt, 0, p.half);
+    // Two pairs of all columns stand together: neighbouring columns read neighbouring 16 bytes.
+    const int pitch = rot_cols * J;
+    rot_table(p, cs, tile.b, tile.t0, tile.nt, pitch, [&](int j) { return (j % J / 2) * rot_cols * 2 + j / J * 2 + (j & 1); });
     __syncthreads();
     if (first >= stride) return;
-    const bool turns = col < rot_cols;
+    const bool turns = col < rot_cols, full = !INTER || col * 4 + 4 <= p.half;
     const int at = turns ? col * 8 : copied0 + (col - rot_cols) * 8;
-    for (int t = 0; t < nt; ++t) {
-        const RotToken tok = rot_token(p, t0 + t);
-        float c[8], s[8];                       // of this column's pairs (interleaved: four)
-        if (turns) {
-#pragma unroll
-            for (int i = 0; i < (INTER ? 4 : 8); ++i) {
-                const int pair = INTER ? col * 4 + i : col * 8 + i;
-                const float2 v = pair < p.half ? cs[t * p.half + pair] : make_float2(1.f, 0.f);
-                c[i] = v.x;
-                s[i] = v.y;
-            }
-        }
-        for (int hb = h0 + first; hb < h1; hb += stride * kAhead) {
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {                  // q, k
+        const int hb = w ? p.H[0] : 0;
+        const int h0 = max(tile.h0, hb) - hb, nh = min(tile.h1 - hb, p.H[w]) - h0;
+        if (nh <= 0) continue;
+        // Rows (token, head), the index whose rows lie closer together first; a step of `stride` rows
+        // is a fixed offset, another when the first index wraps.
+        const bool tok_in = p.xs[w][2] < p.xs[w][1];
+        const int inner = tok_in ? tile.nt : nh, rows = tile.nt * nh;
+        int in = first % inner, out = first / inner;
+        const int in_step = stride % inner, out_step = stride / inner;
+        const int64_t xi = tok_in ? p.xs[w][2] : p.xs[w][1], xo = tok_in ? p.xs[w][1] : p.xs[w][2];
+        const int64_t yi = tok_in ? p.ys[w][2] : p.ys[w][1], yo = tok_in ? p.ys[w][1] : p.ys[w][2];
+        const uint16_t* x = p.x[w] + tile.b * p.xs[w][0] + tile.t0 * p.xs[w][2] + h0 * p.xs[w][1] + in * xi + out * xo + at;
+        uint16_t* y = p.y[w] + tile.b * p.ys[w][0] + tile.t0 * p.ys[w][2] + h0 * p.ys[w][1] + in * yi + out * yo + at;
+        const int64_t x_step = in_step * xi + out_step * xo, x_wrap = xo - inner * xi;
+        const int64_t y_step = in_step * yi + out_step * yo, y_wrap = yo - inner * yi;
+        for (int rw = first; rw < rows; rw += stride * kAhead) {
             uint4 a[kAhead], b[kAhead];
-            RotRow row[kAhead];
+            int token[kAhead];
+            uint16_t* to[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int h = hb + k * stride;
-                if (h >= h1) continue;
-                row[k] = rot_row(p, tok, h);
-                a[k] = *reinterpret_cast<const uint4*>(row[k].x + at);
-                if (!INTER && turns) b[k] = *reinterpret_cast<const uint4*>(row[k].x + p.half + at);
+                if (rw + k * stride < rows) {
+                    a[k] = *reinterpret_cast<const uint4*>(x);
+                    if (!INTER && turns) b[k] = *reinterpret_cast<const uint4*>(x + p.half);
+                }
+                token[k] = tok_in ? in : out;
+                to[k] = y;
+                in += in_step;
+                out += out_step;
+                x += x_step;
+                y += y_step;
+                if (in >= inner) {
+                    in -= inner;
+                    ++out;
+                    x += x_wrap;
+                    y += y_wrap;
+                }
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                if (hb + k * stride >= h1) continue;
+                if (rw + k * stride >= rows) break;
                 if (!turns) {
-                    *reinterpret_cast<uint4*>(row[k].y + at) = a[k];
-                } else if constexpr (INTER) {
-                    uint32_t w[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+                    *reinterpret_cast<uint4*>(to[k]) = a[k];
+                    continue;
+                }
+                const float2* v = cs + token[k] * pitch + col * 2;
+                if constexpr (INTER) {
+                    uint32_t u[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 v = rot_unpack<BF16>(w[i]);
-                        if (col * 4 + i < p.half) w[i] = pack2<BF16>(v.x * c[i] - v.y * s[i], v.y * c[i] + v.x * s[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
+                        const float2 e = rot_unpack<BF16>(u[2 * i]), f = rot_unpack<BF16>(u[2 * i + 1]);
+                        if (full || col * 4 + 2 * i < p.half) u[2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
+                        if (full || col * 4 + 2 * i + 1 < p.half) u[2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
                     }
-                    *reinterpret_cast<uint4*>(row[k].y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(to[k]) = make_uint4(u[0], u[1], u[2], u[3]);
                 } else {
                     float x1[8], x2[8];
                     rot_unpack8<BF16>(a[k], x1);
@@ -148,11 +167,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_columns_kernel(const __gri
                     uint32_t w1[4], w2[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        w1[i] = pack2<BF16>(x1[2 * i] * c[2 * i] - x2[2 * i] * s[2 * i], x1[2 * i + 1] * c[2 * i + 1] - x2[2 * i + 1] * s[2 * i + 1]);
-                        w2[i] = pack2<BF16>(x2[2 * i] * c[2 * i] + x1[2 * i] * s[2 * i], x2[2 * i + 1] * c[2 * i + 1] + x1[2 * i + 1] * s[2 * i + 1]);
+                        const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
+                        w1[i] = pack2<BF16>(x1[2 * i] * q.x - x2[2 * i] * q.y, x1[2 * i + 1] * q.z - x2[2 * i + 1] * q.w);
+                        w2[i] = pack2<BF16>(x2[2 * i] * q.x + x1[2 * i] * q.y, x2[2 * i + 1] * q.z + x1[2 * i + 1] * q.w);
                     }
-                    *reinterpret_cast<uint4*>(row[k].y + at) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                    *reinterpret_cast<uint4*>(row[k].y + p.half + at) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+                    *reinterpret_cast<uint4*>(to[k]) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                    *reinterpret_cast<uint4*>(to[k] + p.half) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
                 }
             }
         }
@@ -164,25 +184,25 @@ template <bool BF16>
 __global__ void __launch_bounds__(kRotThreads) rotary_pairs_kernel(const __grid_constant__ RotaryParams p) {
     __shared__ float2 cs[kRotTable];
     grid_dependency_wait();
-    const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
-    const int nt = (int)min((int64_t)p.tokens_per_cta, (int64_t)p.B * p.S - t0);
-    const int heads = p.H[0] + p.H[1];
-    const int h0 = (int)((int64_t)heads * blockIdx.y / gridDim.y), h1 = (int)((int64_t)heads * (blockIdx.y + 1) / gridDim.y);
-    rot_table(p, cs, t0, nt, 0, p.half);
+    const RotTile tile = rot_tile(p);
+    rot_table(p, cs, tile.b, tile.t0, tile.nt, p.half, [](int j) { return j; });
     __syncthreads();
     const int items = p.half + (p.in_place ? 0 : p.D - 2 * p.half);     // of a row: pairs, then copied elements
-    for (int64_t it = threadIdx.x; it < (int64_t)nt * (h1 - h0) * items; it += kRotThreads) {
+    const int nh = tile.h1 - tile.h0;
+    for (int64_t it = threadIdx.x; it < (int64_t)tile.nt * nh * items; it += kRotThreads) {
         const int j = (int)(it % items), rw = (int)(it / items);
-        const int t = rw / (h1 - h0);
-        const RotRow row = rot_row(p, rot_token(p, t0 + t), h0 + rw - t * (h1 - h0));
+        const int t = rw / nh, head = tile.h0 + rw - t * nh;
+        const int w = head >= p.H[0], h = w ? head - p.H[0] : head, s = tile.t0 + t;
+        const uint16_t* x = p.x[w] + tile.b * p.xs[w][0] + h * p.xs[w][1] + s * p.xs[w][2];
+        uint16_t* y = p.y[w] + tile.b * p.ys[w][0] + h * p.ys[w][1] + s * p.ys[w][2];
         if (j < p.half) {
             const float2 v = cs[t * p.half + j];
-            const float x1 = rot_unpack<BF16>(row.x[j]).x, x2 = rot_unpack<BF16>(row.x[j + p.half]).x;
-            const uint32_t w = pack2<BF16>(x1 * v.x - x2 * v.y, x2 * v.x + x1 * v.y);
-            row.y[j] = (uint16_t)(w & 0xFFFFu);
-            row.y[j + p.half] = (uint16_t)(w >> 16);
+            const float x1 = rot_unpack<BF16>(x[j]).x, x2 = rot_unpack<BF16>(x[j + p.half]).x;
+            const uint32_t u = pack2<BF16>(x1 * v.x - x2 * v.y, x2 * v.x + x1 * v.y);
+            y[j] = (uint16_t)(u & 0xFFFFu);
+            y[j + p.half] = (uint16_t)(u >> 16);
         } else {
-            row.y[j + p.half] = row.x[j + p.half];
+            y[j + p.half] = x[j + p.half];
         }
     }
 }
@@ -191,13 +211,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_pairs_kernel(const __grid_
 
 cudaError_t launch_rotary(const RotaryParams& p0, bool bf16, bool interleaved, int nsm, cudaStream_t st) {
     RotaryParams p = p0;
-    const int64_t tokens = (int64_t)p.B * p.S;
+    p.pos_token_stride = 1;
+    if (p.S == 1) {
+        // One token a sequence: the sequences take the tokens' place.
+        p.S = p.B;
+        p.B = 1;
+        for (int w = 0; w < 2; ++w) {
+            p.xs[w][2] = p.xs[w][0];
+            p.ys[w][2] = p.ys[w][0];
+        }
+        p.pos_token_stride = p.pos ? p.pos_stride : 0;
+    }
     // Tokens a CTA: as the table holds them, up to 16, fewer while that leaves SMs without CTAs.
-    int tt = kRotTable / p.half;
+    int tt = kRotTable / ((p.half + 7) / 8 * 8);
     tt = tt > 16 ? 16 : tt;
-    while (tt > 1 && (tokens + tt - 1) / tt < 4 * nsm) tt /= 2;
+    while (tt > 1 && (int64_t)p.B * ((p.S + tt - 1) / tt) < 4 * nsm) tt /= 2;
     p.tokens_per_cta = tt;
-    const int64_t gx = (tokens + tt - 1) / tt;
+    p.ctas_per_seq = (p.S + tt - 1) / tt;
+    const int64_t gx = (int64_t)p.B * p.ctas_per_seq;       // at most the tokens: fewer than 2^31
     const int heads = p.H[0] + p.H[1];
     int gy = gx < nsm ? (int)((2 * nsm + gx - 1) / gx) : 1;
     gy = gy > heads ? heads : gy;

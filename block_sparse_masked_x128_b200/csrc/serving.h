@@ -29,7 +29,9 @@ struct RotaryParams {
     const double* freq;           // [half] radians a position
     float factor;
     int32_t inverse, in_place;
-    int32_t tokens_per_cta;
+    // Set by launch_rotary.
+    int64_t pos_token_stride;
+    int32_t tokens_per_cta, ctas_per_seq;
 };
 cudaError_t launch_rotary(const RotaryParams& p, bool bf16, bool interleaved, int nsm, cudaStream_t st);
 
