@@ -150,8 +150,8 @@ struct SeqRange {
 __device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int sub) {
     SeqRange r;
     const int n = __ldg(p.kv_lens + b);
-    if ((unsigned)n > (unsigned)p.capacity) g_cache_decode_status = 2;
-    r.len = max(0, min(n, p.capacity));
+    if ((unsigned)n > (unsigned)p.c.capacity) g_cache_decode_status = 2;
+    r.len = max(0, min(n, p.c.capacity));
     r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
     r.tile = r.lo / kTileKeys;
     r.steps = r.len > r.lo ? ((r.len + kTileKeys - 1) / kTileKeys - r.tile + sub - 1) / sub : 0;

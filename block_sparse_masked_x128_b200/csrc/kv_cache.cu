@@ -42,8 +42,8 @@ __device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
 }
 
 // x / scale to the nearest integer, ties to even, exactly (|x / scale| <= 127 (1 + 2^-23)).
-// The product with the rounded inverse is within 2^-15 of x / scale; only where it falls that
-// near a half does the exact sign of x - (r +- 1/2) scale, one fma, decide.
+// x times `inv`, which is within 2^-22 of 1 / scale, is within 2^-15 + 2^-18 of x / scale; only where
+// it falls within 10^-4 of a half does the exact sign of x - (r +- 1/2) scale, one fma, decide.
 __device__ __forceinline__ int quantise_s8(float x, float scale, float inv) {
     float r = rintf(x * inv);
     if (fabsf(fmaf(x, inv, -r)) > 0.4999f) {
@@ -79,6 +79,17 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
+// The bits, as fp32, of the largest magnitude of a row whose 16-bit values are spread over LPR
+// lanes, eight each: magnitudes order as their bits, two at a time.
+template <bool BF16, int LPR>
+__device__ __forceinline__ uint32_t row_amax(const uint4& r) {
+    uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, off));
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);
+    return BF16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
+}
+
 // The code bytes of a row's eight values and its scale; `amax` holds the bits of its largest
 // magnitude.
 template <int DT>
@@ -86,7 +97,8 @@ __device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t amax
     scale = row_scale<DT>(amax);
     uint32_t c[2] = {0u, 0u};
     if (amax < 0x7f800000u) {
-        const float inv = __frcp_rn(scale);
+        // e4m3: the scale is a power of two, its inverse exact.  s8: within 2^-22 of 1 / scale.
+        const float inv = DT == FA_DTYPE_E4M3 ? __uint_as_float(0x7f000000u - __float_as_uint(scale)) : __fdividef(1.f, scale);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t two;
@@ -110,7 +122,10 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
     const int count = p.limit ? min(__ldg(p.limit + b), p.S) : p.S;
-    const int64_t start = __ldg(p.start + b);
+    if ((int)(blockIdx.x * RPC * kRowsAhead) >= count) return;
+    // A position start + s, as 32 bits without sign: past the capacity where it is negative.
+    const uint32_t start = __ldg(p.start + b);
+    const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
     uint4 raw[kRowsAhead][2];
     int page[kRowsAhead];
 #pragma unroll
@@ -122,14 +137,13 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
 #pragma unroll
             for (int w = 0; w < 2; ++w)
                 raw[i][w] = *reinterpret_cast<const uint4*>(p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8);
-            const int64_t pos = start + s;
-            page[i] = pos < 0 ? -1 : cache_page(p.c, b, pos >> p.c.page_shift);
-            if (page[i] < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+            page[i] = cache_page(p.c, table, start + s);
+            if (page[i] < 0) g_cache_rows_status = 2;
         }
     }
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
-        const int row = (int)((start + s0 + i * RPC) & ((1 << p.c.page_shift) - 1));
+        const int row = (start + s0 + i * RPC) & ((1 << p.c.page_shift) - 1);
         const int64_t at = (int64_t)page[i] * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
         const int64_t sat = (int64_t)page[i] * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
 #pragma unroll
@@ -140,11 +154,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
             } else {
                 float x[8];
                 row_unpack<BF16>(raw[i][w], x);
-                uint32_t m = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-                for (int off = LPR / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, off));
+                const uint32_t m = row_amax<BF16, LPR>(raw[i][w]);
                 float scale;
                 const uint2 c = quantise_row<DT>(x, m, scale);
                 if (page[i] >= 0) {
@@ -164,19 +174,20 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
     const int sub = threadIdx.x % LPR;
     const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
-    const int64_t start = p.start ? (int64_t)__ldg(p.start + b) : 0;
+    const uint32_t start = p.start ? __ldg(p.start + b) : 0;
     const int len = __ldg(p.limit + b);
+    const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
     uint4 raw[kRowsAhead][2];
     float scale[kRowsAhead][2];
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
-        const int64_t pos = start + s0 + i * RPC;
+        const uint32_t pos = start + s0 + i * RPC;      // as in the append
         int page = -1;
-        if (s0 + i * RPC < p.S && pos >= 0 && pos < len) {
-            page = cache_page(p.c, b, pos >> p.c.page_shift);
-            if (page < 0 && sub == 0 && h == 0) atomicExch(&g_cache_rows_status, 2);
+        if (s0 + i * RPC < p.S && (int)pos >= 0 && (int)pos < len) {
+            page = cache_page(p.c, table, pos);
+            if (page < 0) g_cache_rows_status = 2;
         }
-        const int row = (int)(pos & ((1 << p.c.page_shift) - 1));
+        const int row = pos & ((1 << p.c.page_shift) - 1);
         const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
         const int64_t sat = (int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
 #pragma unroll

@@ -47,6 +47,7 @@ struct CacheView {
     const int32_t* table;         // [B][table_stride] page of each block of the sequence
     int64_t table_stride;
     int32_t table_width;
+    int32_t capacity;             // tokens that a row of the table maps, at most 2^31 - 64
 };
 
 struct CacheRowsParams {
@@ -71,7 +72,6 @@ struct CacheDecodeParams {
     int32_t B, HQ, group;         // group = query heads a kv head
     const int32_t* kv_lens;       // [B]
     int32_t window;               // 0: all keys
-    int32_t capacity;             // tokens that a page table row maps
     float scale_log2, softcap_log2, softcap_k;   // softcap_k: 2 / softcap
     const float* alibi_slopes;
     int32_t score_kind;
@@ -108,11 +108,11 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The page of block `blk` of sequence b, or -1 where the table has none or an index outside
-// the pool.
-__device__ __forceinline__ int cache_page(const CacheView& c, int b, int64_t blk) {
-    if (blk < 0 || blk >= c.table_width) return -1;
-    const int page = __ldg(c.table + (int64_t)b * c.table_stride + blk);
+// The page of position `pos` (32 bits without sign) by a sequence's row of the table, or -1 where
+// the row does not reach it or names a page outside the pool.
+__device__ __forceinline__ int cache_page(const CacheView& c, const int32_t* table, uint32_t pos) {
+    if (pos >= (uint32_t)c.capacity) return -1;
+    const int page = __ldg(table + (pos >> c.page_shift));
     return (unsigned)page < (unsigned)c.n_pages ? page : -1;
 }
 #endif

@@ -93,6 +93,9 @@ fa_status_t check_cache(const fa_kv_cache_t* c, const int32_t* table, int64_t ta
     view->table = table;
     view->table_stride = table_stride;
     view->table_width = (int32_t)table_width;
+    // The kernels count tokens in 32 bits.
+    const int64_t capacity = table_width << view->page_shift;
+    view->capacity = (int32_t)(capacity < 0x7fffffc0 ? capacity : 0x7fffffc0);
     return FA_OK;
 }
 
@@ -360,9 +363,6 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     p.group = (int32_t)(q->H / cache->H);
     p.kv_lens = kv_lens;
     p.window = window;
-    // The kernels count keys in 32 bits (2^31 - 64 tokens a sequence at most).
-    const int64_t capacity = table_width << p.c.page_shift;
-    p.capacity = (int32_t)(capacity < 0x7fffffc0 ? capacity : 0x7fffffc0);
     p.scale_log2 = (float)(sc * log2e);
     p.softcap_log2 = (float)(cap * log2e);
     p.softcap_k = (float)(2.0 / cap);
