@@ -16,6 +16,8 @@
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 namespace fa {
@@ -41,18 +43,38 @@ __device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
     }
 }
 
-// x / scale to the nearest integer, ties to even, exactly (|x / scale| <= 127 (1 + 2^-23)).
-// x times `inv`, which is within 2^-22 of 1 / scale, is within 2^-15 + 2^-18 of x / scale; only where
-// it falls within 10^-4 of a half does the exact sign of x - (r +- 1/2) scale, one fma, decide.
-__device__ __forceinline__ int quantise_s8(float x, float scale, float inv) {
+// x / scale to the nearest integer, ties to even, exactly (|x / scale| <= 127 (1 + 2^-23)).  x times
+// `inv`, which is within 2^-22 of 1 / scale, is within 2^-15 + 2^-18 of x / scale, so rounding the
+// product is right unless it falls that near a half; the rows where one does within 10^-4 decide by
+// the exact sign of x - (r +- 1/2) scale, one fma.
+__device__ __forceinline__ int quantise_s8_exactly(float x, float scale, float inv) {
     float r = rintf(x * inv);
-    if (fabsf(fmaf(x, inv, -r)) > 0.4999f) {
-        const float up = fmaf(-(r + 0.5f), scale, x), down = fmaf(-(r - 0.5f), scale, x);
-        const bool odd = ((int)r & 1) != 0;
-        if (up > 0.f || (up == 0.f && odd)) r += 1.f;
-        else if (down < 0.f || (down == 0.f && odd)) r -= 1.f;
-    }
+    const float up = fmaf(-(r + 0.5f), scale, x), down = fmaf(-(r - 0.5f), scale, x);
+    const bool odd = ((int)r & 1) != 0;
+    if (up > 0.f || (up == 0.f && odd)) r += 1.f;
+    else if (down < 0.f || (down == 0.f && odd)) r -= 1.f;
     return (int)r;
+}
+
+__device__ __forceinline__ uint2 quantise_s8x8(const float (&x)[8], float scale, float inv) {
+    constexpr float kMagic = 12582912.f;        // 1.5 * 2^23: its unit is 1, so adding it rounds to an integer
+    uint32_t c[8];
+    float near = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float m = fmaf(x[i], inv, kMagic);
+        c[i] = __float_as_uint(m);              // the low byte is the code
+        near = fmaxf(near, fabsf(fmaf(x[i], inv, kMagic - m)));
+    }
+    if (near > 0.4999f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = (uint32_t)quantise_s8_exactly(x[i], scale, inv);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+    return make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ uint32_t quantise_e4m3x2(float lo, float hi) {
@@ -95,28 +117,19 @@ __device__ __forceinline__ uint32_t row_amax(const uint4& r) {
 template <int DT>
 __device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t amax, float& scale) {
     scale = row_scale<DT>(amax);
-    uint32_t c[2] = {0u, 0u};
-    if (amax < 0x7f800000u) {
-        // e4m3: the scale is a power of two, its inverse exact.  s8: within 2^-22 of 1 / scale.
-        const float inv = DT == FA_DTYPE_E4M3 ? __uint_as_float(0x7f000000u - __float_as_uint(scale)) : __fdividef(1.f, scale);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t two;
-            if constexpr (DT == FA_DTYPE_S8)
-                two = (uint32_t)(quantise_s8(x[2 * i], scale, inv) & 0xFF) | (uint32_t)(quantise_s8(x[2 * i + 1], scale, inv) & 0xFF) << 8;
-            else
-                two = quantise_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-            c[i / 2] |= two << (16 * (i % 2));
-        }
-    }
-    return make_uint2(c[0], c[1]);
+    if (amax >= 0x7f800000u) return make_uint2(0u, 0u);
+    if constexpr (DT == FA_DTYPE_S8) return quantise_s8x8(x, scale, __fdividef(1.f, scale));
+    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(scale));       // exact: a power of two
+    return make_uint2(quantise_e4m3x2(x[0] * inv, x[1] * inv) | quantise_e4m3x2(x[2] * inv, x[3] * inv) << 16,
+                      quantise_e4m3x2(x[4] * inv, x[5] * inv) | quantise_e4m3x2(x[6] * inv, x[7] * inv) << 16);
 }
 
 // Grid (ceil(S / (groups kRowsAhead)), H, B): a group of D / 8 lanes takes kRowsAhead rows, all
 // loaded before the first is worked on.
 template <int DT, int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheRowsParams p) {
-    constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    constexpr int LPR = D / 8;
+    const int RPC = blockDim.x / LPR;
     grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
     const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
@@ -143,6 +156,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     }
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i) {
+        if (!__any_sync(kFullMask, page[i] >= 0)) continue;
         const int row = (start + s0 + i * RPC) & ((1 << p.c.page_shift) - 1);
         const int64_t at = (int64_t)page[i] * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
         const int64_t sat = (int64_t)page[i] * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
@@ -169,7 +183,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
 // Rows start .. start + S - 1 of each sequence; those past its length are zero.
 template <int DT, int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
-    constexpr int LPR = D / 8, RPC = kRowThreads / LPR;
+    constexpr int LPR = D / 8;
+    const int RPC = blockDim.x / LPR;
     grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
     const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
@@ -232,9 +247,10 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
 
 template <int DT, int D, bool BF16>
 cudaError_t launch_rows(const CacheRowsParams& p, bool append, cudaStream_t st) {
-    constexpr int RPC = kRowThreads / (D / 8);
-    constexpr int rows = RPC * kRowsAhead;
-    const dim3 grid((unsigned)((p.S + rows - 1) / rows), (unsigned)p.c.H, (unsigned)p.B), block(kRowThreads);
+    // A warp is enough for a step's single rows; a block's other warps would only be in the way.
+    const int warps = (int)std::min<int64_t>(kRowThreads / 32, ((int64_t)p.S * (D / 8) + 31) / 32);
+    const int rows = warps * 32 / (D / 8) * kRowsAhead;
+    const dim3 grid((unsigned)((p.S + rows - 1) / rows), (unsigned)p.c.H, (unsigned)p.B), block(warps * 32);
     return append ? launch_early(cache_append_kernel<DT, D, BF16>, grid, block, 0, st, p)
                   : launch_early(cache_read_kernel<DT, D, BF16>, grid, block, 0, st, p);
 }
