@@ -12,9 +12,7 @@ FlexAttention API the pages use ("How to Use FlexAttention on Apple Silicon", Se
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
 from typing import Optional, Tuple
 
 # FA_B200_LIBRARY may name another build of the same library (build.py --debug writes
@@ -155,7 +153,7 @@ _lib.fa_backward.argtypes = [ctypes.POINTER(FaTensor)] * 5 + [
 _lib.fa_backward.restype = _status
 
 # The serving calls take their descriptions (fa_tensor_t, fa_kv_cache_t, ...) as addresses: a packed
-# bytes object (_packed below) or a byref() alike.
+# bytes object or a byref() alike.
 _p, _i64 = ctypes.c_void_p, ctypes.c_int64
 _lib.fa_rotary_frequencies.argtypes = [ctypes.c_int32, ctypes.c_double, _p, _p]
 _lib.fa_rotary.argtypes = [_p, _p, _p, _i64, _i64, _p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
@@ -581,238 +579,17 @@ def masked_softmax(scores, offset: Optional[int] = None, *, causal: bool = True,
 
 
 # ---------------------------------------------------------------- serving: rotary, cache, decode
+#
+# serving.py imports torch, so it is loaded when one of its names is first asked for.
 
-# These calls are short, a decode step has several, and the GPU waits for the host between them:
-# the descriptions are packed in one go (fa_tensor_t: address, dtype, padding, four extents, four
-# strides) and the current stream is asked for as a bare pointer.
-_packed_tensor = struct.Struct("=Qi4x8q").pack
-
-
-def _packed(t) -> bytes:
-    """fa_tensor(t) as bytes."""
-    shape = t.shape
-    if len(shape) != 4:
-        raise ValueError("expected a (B, H, S, D) tensor")
-    return _packed_tensor(t.data_ptr(), _dtype_code(t.dtype), *shape, *t.stride())
+_SERVING = ("PagedKVCache", "cache_append", "cache_read", "cache_status", "decode_attention",
+            "decode_workspace_bytes", "rotary", "rotary_backward", "rotary_frequencies")
 
 
-def _call(name: str, device, stream, *args) -> None:
-    """_lib.name(*args, stream) with `device` current."""
-    import torch
-    index = device.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(name, device, stream, *args)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
-    status = getattr(_lib, name)(*args, stream)
-    if status != FA_OK:
-        raise FaError(status, name)
-
-
-def _int32_rows(t, name: str, device, n: int):
-    """Raise ValueError unless t is a contiguous int32 CUDA tensor of n values on `device`."""
-    import torch
-    if not (t.dtype == torch.int32 and t.shape == (n,) and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape ({n},) on {device}")
-    return t.data_ptr()
-
-
-def rotary_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: int = FA_ROTARY_SCALE_NONE,
-                       factor: float = 1.0, original_len: float = 0.0, low_turns: float = 1.0,
-                       high_turns: float = 32.0, device=None):
-    """Angles a position (radians) of the rot_dim / 2 pairs, for rotary(): base^(-2i / rot_dim), scaled
-    for long contexts as the FA_ROTARY_SCALE_* kind says.  A float64 tensor on `device` (default: the
-    current CUDA device)."""
-    import torch
-    out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
-    sc = FaRotaryScaling(int(scaling), float(factor), float(original_len), float(low_turns), float(high_turns))
-    _check(_lib.fa_rotary_frequencies(int(rot_dim), float(base), ctypes.byref(sc), out.data_ptr()),
-           "fa_rotary_frequencies")
-    return out.to(device if device is not None else torch.device("cuda", torch.cuda.current_device()))
-
-
-def rotary(q, k, positions, frequencies, *, interleaved: bool = False, factor: float = 1.0, q_out=None,
-           k_out=None, inverse: bool = False, stream=None) -> Tuple:
-    """Rotary positions of q (B, Hq, S, D) and k (B, Hk, S, D; may be None): the pairs of the first
-    2 * len(frequencies) elements of each head turn by position * frequency, times `factor`; the rest
-    is copied.  positions: int32 CUDA tensor (B, S) or (S,), or the int position of row 0.  q_out and
-    k_out may be q and k (in place).  Returns (q_out, k_out)."""
-    import torch
-    dev = q.device
-    if not q.is_cuda or (k is not None and k.device != dev):
-        raise ValueError("q and k must be CUDA tensors of one device")
-    if not (frequencies.dtype == torch.float64 and frequencies.dim() == 1 and frequencies.is_contiguous()
-            and frequencies.device == dev):
-        raise ValueError("frequencies must be a contiguous 1-D float64 tensor on q's device")
-    pos_ptr, pos_stride, pos0 = None, 0, 0
-    if isinstance(positions, int):
-        pos0 = positions
-    else:
-        B, S = q.shape[0], q.shape[2]
-        shape = tuple(positions.shape)
-        if not (positions.dtype == torch.int32 and positions.device == dev and shape in ((S,), (B, S))
-                and (S <= 1 or positions.stride(-1) == 1)):
-            raise ValueError("positions must be an int or an int32 tensor (B, S) or (S,) with contiguous rows on "
-                             "q's device")
-        pos_ptr = positions.data_ptr()
-        pos_stride = positions.stride(0) if len(shape) == 2 and B > 1 else 0
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    if k is not None and k_out is None:
-        k_out = torch.empty_like(k)
-    for t, what in ((q_out, "q_out"), (k_out, "k_out")):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what} must be on q's device")
-    _call("fa_rotary", dev, stream, _packed(q), _packed(k) if k is not None else None, pos_ptr, pos_stride, pos0,
-          frequencies.data_ptr(), 2 * frequencies.numel(), FA_ROTARY_INTERLEAVED if interleaved else FA_ROTARY_HALF,
-          factor, 1 if inverse else 0, _packed(q_out), _packed(k_out) if k_out is not None else None)
-    return q_out, k_out
-
-
-def rotary_backward(dq, dk, positions, frequencies, *, interleaved: bool = False, factor: float = 1.0,
-                    q_out=None, k_out=None, stream=None) -> Tuple:
-    """Gradients of rotary() with respect to its q and k, given those of its outputs."""
-    return rotary(dq, dk, positions, frequencies, interleaved=interleaved, factor=factor, q_out=q_out, k_out=k_out,
-                  inverse=True, stream=stream)
-
-
-class PagedKVCache:
-    """The pools of a paged K/V cache: k and v (n_pages, H, page_size, D) of float16, bfloat16,
-    float8_e4m3fn or int8, any strides whose last is 1 (a transposed (n_pages, page_size, H, D) pool
-    fits), and for the 8-bit types the float32 scales (n_pages, H, page_size).  The tensors stay the
-    caller's; the object keeps them alive and describes them to the library."""
-
-    def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
-        codes = {torch.float16: FA_DTYPE_F16, torch.bfloat16: FA_DTYPE_BF16,
-                 torch.float8_e4m3fn: FA_DTYPE_E4M3, torch.int8: FA_DTYPE_S8}
-        if k.dtype not in codes:
-            raise TypeError(f"unsupported cache dtype {k.dtype}")
-        if not (k.dim() == 4 and k.is_cuda and k.stride(3) == 1 and v.dtype == k.dtype and v.shape == k.shape
-                and v.stride() == k.stride() and v.device == k.device):
-            raise ValueError("k and v must be (n_pages, H, page_size, D) CUDA tensors of one dtype, shape, stride and "
-                             "device, contiguous in D")
-        eight = k.dtype in (torch.float8_e4m3fn, torch.int8)
-        st = (0, 0, 0)
-        if eight:
-            for t in (k_scale, v_scale):
-                if not (t is not None and t.dtype == torch.float32 and t.shape == k.shape[:3] and t.device == k.device
-                        and t.stride() == k_scale.stride()):
-                    raise ValueError("an 8-bit cache needs float32 scales (n_pages, H, page_size) of one stride on "
-                                     "its device")
-            st = k_scale.stride()
-        elif k_scale is not None or v_scale is not None:
-            raise ValueError("a 16-bit cache has no scales")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.dtype, self.device, self.quantised = k.dtype, k.device, eight
-        self.n_pages, self.H, self.page_size, self.D = k.shape
-        self._c = FaKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if eight else None,
-                            v_scale.data_ptr() if eight else None, codes[k.dtype], self.page_size, self.n_pages, self.H,
-                            self.D, (ctypes.c_int64 * 3)(*k.stride()[:3]), (ctypes.c_int64 * 3)(*st))
-        self._ref = ctypes.byref(self._c)
-
-    @classmethod
-    def empty(cls, n_pages: int, H: int, page_size: int, D: int, dtype, device=None):
-        """Fresh pools (zeros), with scales where the type has them."""
-        import torch
-        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        k, v = (torch.zeros(n_pages, H, page_size, D, dtype=dtype, device=dev) for _ in range(2))
-        if dtype in (torch.float8_e4m3fn, torch.int8):
-            return cls(k, v, *(torch.zeros(n_pages, H, page_size, dtype=torch.float32, device=dev) for _ in range(2)))
-        return cls(k, v)
-
-    def _table(self, page_table, B: int):
-        import torch
-        if not (page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == B
-                and page_table.device == self.device and (page_table.shape[1] <= 1 or page_table.stride(1) == 1)):
-            raise ValueError(f"page_table must be an int32 tensor ({B}, n) with contiguous rows on the cache's device")
-        width = page_table.shape[1]
-        return page_table.data_ptr(), (page_table.stride(0) if B > 1 else width), width
-
-
-def cache_append(cache: PagedKVCache, k, v, page_table, start, *, count=None, stream=None) -> None:
-    """Write the new rows k, v (B, H, S, D) of each sequence at positions start[b] + s of the cache
-    (quantised for 8-bit caches); count (int32, B) says how many of a padded batch's S rows are real."""
-    dev, B = cache.device, k.shape[0]
-    if k.device != dev or v.device != dev:
-        raise ValueError("k and v must be on the cache's device")
-    table = cache._table(page_table, B)
-    start_ptr = _int32_rows(start, "start", dev, B)
-    count_ptr = _int32_rows(count, "count", dev, B) if count is not None else None
-    _call("fa_cache_append", dev, stream, _packed(k), _packed(v), cache._ref, *table, start_ptr, count_ptr)
-
-
-def cache_read(cache: PagedKVCache, page_table, kv_lens, S: int, *, start=None, dtype=None, k_out=None,
-               v_out=None, stream=None) -> Tuple:
-    """Rows start[b] .. start[b] + S - 1 (start None: from 0) of each sequence as (k, v) of shape
-    (B, H, S, D); rows at or past kv_lens[b] are zero.  dtype: of the result (a 16-bit cache's own;
-    bfloat16 by default for 8-bit caches)."""
-    import torch
-    dev, B = cache.device, page_table.shape[0]
-    if dtype is None:
-        dtype = torch.bfloat16 if cache.quantised else cache.dtype
-    outs = [torch.empty(B, cache.H, int(S), cache.D, dtype=dtype, device=dev) if t is None else t for t in (k_out, v_out)]
-    for t in outs:
-        if t.device != dev or tuple(t.shape) != (B, cache.H, int(S), cache.D):
-            raise ValueError("k_out and v_out must be (B, H, S, D) tensors on the cache's device")
-    table = cache._table(page_table, B)
-    lens_ptr = _int32_rows(kv_lens, "kv_lens", dev, B)
-    start_ptr = _int32_rows(start, "start", dev, B) if start is not None else None
-    _call("fa_cache_read", dev, stream, cache._ref, *table, start_ptr, lens_ptr, _packed(outs[0]), _packed(outs[1]))
-    return tuple(outs)
-
-
-def decode_workspace_bytes(B: int, HQ: int, H: int, D: int) -> int:
-    return int(_lib.fa_decode_workspace_bytes(B, HQ, H, D))
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_workspace(device, B: int, HQ: int, H: int, D: int) -> int:
-    import torch
-    with torch.cuda.device(device):
-        return decode_workspace_bytes(B, HQ, H, D)
-
-
-def decode_attention(q, cache: PagedKVCache, page_table, kv_lens, *, window: int = 0,
-                     score_mod: int = FA_SCORE_NONE, softcap: float = 30.0, alibi_slopes=None,
-                     scale: Optional[float] = None, out=None, lse=None, return_lse: bool = True, workspace=None,
-                     stream=None) -> Tuple:
-    """Attention of one new token a sequence: q (B, HQ, 1, D) over the kv_lens[b] (int32, the new one
-    among them) tokens that page_table maps, or the last `window` of them; HQ a multiple of the cache's
-    heads.  The lengths are read on the device.  Returns (out, lse), lse (B, HQ, 1) or None."""
-    import torch
-    dev = cache.device
-    if q.device != dev:
-        raise ValueError("q must be on the cache's device")
-    B, HQ = q.shape[0], q.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.device != dev:
-        raise ValueError("out must be on the cache's device")
-    if lse is None:
-        if return_lse:
-            lse = torch.empty(B, HQ, 1, device=dev, dtype=torch.float32)
-    elif not (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (B, HQ, 1) and lse.device == dev):
-        raise ValueError("lse must be a contiguous float32 tensor (B, HQ, 1) on the cache's device")
-    table = cache._table(page_table, B)
-    lens_ptr = _int32_rows(kv_lens, "kv_lens", dev, B)
-    params = None
-    if score_mod:
-        params = ctypes.byref(FaScoreParams(float(softcap), _check_alibi(alibi_slopes, q)))
-    if workspace is None:
-        workspace = torch.empty(_decode_workspace(dev, B, HQ, cache.H, cache.D), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError("workspace must be on the cache's device")
-    _call("fa_decode", dev, stream, _packed(q), cache._ref, *table, lens_ptr, window, score_mod, params,
-          scale if scale is not None else -1.0, _packed(out), lse.data_ptr() if lse is not None else None,
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return out, lse
-
-
-def cache_status(stream=None) -> int:
-    """Synchronise the stream and return FA_OK, or FA_ERR_INVALID_ARG when a call on a cache of the
-    current device met a page, position or length out of range since the last look."""
-    return _lib.fa_cache_status(_stream_ptr(stream))
+def __getattr__(name: str):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
