@@ -4,6 +4,7 @@
 
 (Run it as a file, not as a package module: importing the package loads the library.)
 
+Beside it goes _lib/fa_b200_torch.so, the host path of the serving calls (g++ against torch's headers).
 Each .cu file is compiled to an object in parallel (nvcc cross-compiles for sm_100a without
 a GPU), then linked into one shared library exporting the C ABI of include/fa_b200.h.
 Objects are rebuilt only when a source or header is newer.  `--ptxas-info` prints the
@@ -28,6 +29,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfa_b200.so")
 TRACE_LIB = os.path.join(LIBDIR, "libfa_b200_trace.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libfa_b200_debug.so")
+BINDING = os.path.join(LIBDIR, "fa_b200_torch.so")      # the serving calls' host path (csrc/binding.cpp)
 SOURCES = ["api.cu", "mask_builder.cu", "attn_fwd.cu", "noalloc.cu", "masked_softmax.cu", "attn_bwd.cu", "decode.cu",
            "serving_api.cu", "rotary.cu", "kv_cache.cu", "decode_cache.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -70,6 +72,29 @@ def _compile(src: str, flags: list, force: bool, build_dir: str = BUILD) -> tupl
     return obj, r.stdout + r.stderr
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp, the Python extension that takes torch tensors to the C ABI."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "fa_b200.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    os.makedirs(LIBDIR, exist_ok=True)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), src, "-o", BINDING,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return BINDING
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
           trace: bool = False, debug: bool = False) -> str:
     """Build the library; trace=True builds the phase-tracing variant, debug=True the variant
@@ -80,8 +105,10 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
     os.makedirs(build_dir, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     flags = _flags(ptxas_info, trace, debug)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(lambda s: _compile(s, flags, force or ptxas_info, build_dir), SOURCES))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_info:
         for _, log in results:
