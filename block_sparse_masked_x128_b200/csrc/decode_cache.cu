@@ -44,7 +44,6 @@ namespace {
 __device__ int32_t g_cache_decode_status;   // 2: a length or page out of range was met
 
 constexpr int kCdWarps = 4, kCdThreads = 32 * kCdWarps;
-constexpr int kMergeThreads = 512;
 constexpr int kTileKeys = 16;               // keys a warp takes at a time
 constexpr float kCdLn2 = 0.6931471805599453f, kCdLog2e = 1.4426950408889634f;
 constexpr float kTopWeight = 256.f;         // weights above this raise the reference
@@ -662,87 +661,146 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     grid_dependency_release();
 }
 
-// One CTA a (sequence, query head): joins the parts of a head whose keys several warps shared, in
-// key order; and writes the result of a sequence without keys.
-template <int D, int SLICES>
-__global__ void __launch_bounds__(kMergeThreads) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
-    constexpr int DS = D / SLICES, LPR = DS / 4, WARPS = kMergeThreads / 32;     // dims of this CTA
-    __shared__ __align__(16) float s_o[WARPS][DS];      // written as float4
-    __shared__ float s_l[WARPS], s_m[WARPS];
-    const int b = blockIdx.x / p.HQ, hq = blockIdx.x - b * p.HQ;
-    const int CB = col_blocks(p.group, cols);
-    const int h = hq / p.group, g = hq - h * p.group, cb = g / cols, col = g % cols;
-    grid_dependency_wait();
-    const bool none = seq_range(p, b, sub).steps == 0;
-    const int2 head = none ? make_int2(0, 0) : p.heads[((int64_t)b * p.c.H + h) * CB + cb];
-    const int pieces = head.x;
-    if (pieces == 1) return;        // its warp wrote the result
-    // Each group of lanes joins every groups-th part, kAhead of them loaded at a time: the parts are
-    // in L2, so their latency is the cost.  The first is in slot head.y, the others are the first
-    // of the following workers of this block of columns.
-    constexpr int kAhead = 4;
-    const int groups = blockDim.x / LPR, grp = threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
-    const int64_t step = (int64_t)2 * CB;
-    float M = -FLT_MAX, L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = grp; k0 < pieces; k0 += groups * kAhead) {
+// ---- the merge: joins the parts of a head whose keys several warps shared, in key order, and writes
+// the result of a sequence without keys.  The parts are in L2, so latency is its cost: a group of
+// D / 4 lanes takes every stride-th part, kAhead of them loaded at a time.
+
+struct Joined {
+    float M, L;
+    float4 O;
+};
+__device__ __forceinline__ Joined join(const Joined& a, const Joined& b) {
+    const float M = fmaxf(a.M, b.M), fa = ex2_approx(a.M - M), fb = ex2_approx(b.M - M);
+    return {M, a.L * fa + b.L * fb, make_float4(a.O.x * fa + b.O.x * fb, a.O.y * fa + b.O.y * fb, a.O.z * fa + b.O.z * fb, a.O.w * fa + b.O.w * fb)};
+}
+
+// A query head: its parts, the first one's slot (the others are the first slots of the following
+// workers of its block of columns), and its column there.
+struct MergeHead {
+    int b, hq, col, parts, slot;
+};
+__device__ __forceinline__ MergeHead merge_head(const CacheDecodeParams& p, int64_t i, int cols, int sub) {
+    MergeHead m;
+    m.b = (int)(i / p.HQ);
+    m.hq = (int)(i - (int64_t)m.b * p.HQ);
+    const int CB = col_blocks(p.group, cols), h = m.hq / p.group, g = m.hq - h * p.group, cb = g / cols;
+    m.col = g - cb * cols;
+    const int2 e = p.heads[((int64_t)m.b * p.c.H + h) * CB + cb];      // nobody's, where there are no keys
+    const bool none = seq_range(p, m.b, sub).steps == 0;
+    m.parts = none ? 0 : e.x;
+    m.slot = e.y;
+    return m;
+}
+
+template <int D, int kAhead>
+__device__ __forceinline__ Joined join_parts(const CacheDecodeParams& p, const MergeHead& m, int cols, int first, int stride, int d) {
+    const int64_t step = (int64_t)2 * col_blocks(p.group, cols);
+    Joined r = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = first; k0 < m.parts; k0 += stride * kAhead) {
         float2 ml[kAhead];
         float4 v[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int k = k0 + i * groups;
+            const int k = k0 + i * stride;
             ml[i] = make_float2(-FLT_MAX, 0.f);
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < pieces) {
-                const float* po = p.partials + (k == 0 ? (int64_t)head.y : (head.y & ~1) + k * step) * cols * (D + 2);
-                ml[i] = *reinterpret_cast<const float2*>(po + cols * D + 2 * col);
-                v[i] = *reinterpret_cast<const float4*>(po + col * D + blockIdx.y * DS + d);
+            if (k < m.parts) {
+                const float* po = p.partials + (k == 0 ? (int64_t)m.slot : (m.slot & ~1) + k * step) * cols * (D + 2);
+                ml[i] = *reinterpret_cast<const float2*>(po + cols * D + 2 * m.col);
+                v[i] = *reinterpret_cast<const float4*>(po + m.col * D + d);
             }
         }
-        float Mn = M;
+        float M = r.M;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) Mn = fmaxf(Mn, ml[i].x);
-        const float a = ex2_approx(M - Mn);
-        M = Mn;
-        L *= a;
-        O = make_float4(O.x * a, O.y * a, O.z * a, O.w * a);
+        for (int i = 0; i < kAhead; ++i) M = fmaxf(M, ml[i].x);
+        const float a = ex2_approx(r.M - M);
+        r = {M, r.L * a, make_float4(r.O.x * a, r.O.y * a, r.O.z * a, r.O.w * a)};
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const float f = ex2_approx(ml[i].x - M);
-            L = fmaf(ml[i].y, f, L);
-            O = make_float4(fmaf(v[i].x, f, O.x), fmaf(v[i].y, f, O.y), fmaf(v[i].z, f, O.z), fmaf(v[i].w, f, O.w));
+            r.L = fmaf(ml[i].y, f, r.L);
+            r.O = make_float4(fmaf(v[i].x, f, r.O.x), fmaf(v[i].y, f, r.O.y), fmaf(v[i].z, f, r.O.z), fmaf(v[i].w, f, r.O.w));
         }
     }
-    // The groups of a warp, then the warps.
+    return r;
+}
+
+// The groups of LPR lanes of a warp together: every lane gets the whole of its dims.
+template <int LPR>
+__device__ __forceinline__ Joined join_warp(Joined r) {
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
-        const float Mo = __shfl_xor_sync(kFullMask, M, off), Lo = __shfl_xor_sync(kFullMask, L, off);
-        const float Mn = fmaxf(M, Mo), fa = ex2_approx(M - Mn), fb = ex2_approx(Mo - Mn);
-        M = Mn;
-        L = L * fa + Lo * fb;
-        O.x = O.x * fa + __shfl_xor_sync(kFullMask, O.x, off) * fb;
-        O.y = O.y * fa + __shfl_xor_sync(kFullMask, O.y, off) * fb;
-        O.z = O.z * fa + __shfl_xor_sync(kFullMask, O.z, off) * fb;
-        O.w = O.w * fa + __shfl_xor_sync(kFullMask, O.w, off) * fb;
+        Joined o;
+        o.M = __shfl_xor_sync(kFullMask, r.M, off);
+        o.L = __shfl_xor_sync(kFullMask, r.L, off);
+        o.O.x = __shfl_xor_sync(kFullMask, r.O.x, off);
+        o.O.y = __shfl_xor_sync(kFullMask, r.O.y, off);
+        o.O.z = __shfl_xor_sync(kFullMask, r.O.z, off);
+        o.O.w = __shfl_xor_sync(kFullMask, r.O.w, off);
+        r = join(r, o);
     }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if (lane < LPR) *reinterpret_cast<float4*>(&s_o[warp][d]) = O;
-    if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = L;
-    }
+    return r;
+}
+
+__device__ __forceinline__ void write_joined(const CacheDecodeParams& p, bool q_bf16, const MergeHead& m, const Joined& r, int d) {
+    const float inv = r.L == 0.f ? 0.f : 1.f / r.L;
+    uint2 w = q_bf16 ? make_uint2(pack2<true>(r.O.x * inv, r.O.y * inv), pack2<true>(r.O.z * inv, r.O.w * inv))
+                     : make_uint2(pack2<false>(r.O.x * inv, r.O.y * inv), pack2<false>(r.O.z * inv, r.O.w * inv));
+    if (r.L == 0.f) w = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(p.out + m.b * p.out_stride[0] + (int64_t)m.hq * p.out_stride[1] + d) = w;
+    if (d == 0 && p.lse) p.lse[(int64_t)m.b * p.HQ + m.hq] = r.L == 0.f ? -INFINITY : (r.M + log2f(r.L)) * kCdLn2;
+}
+
+// SLICES CTAs of WARPS warps a head, D / SLICES dims each.
+template <int D, int SLICES, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) cache_decode_merge_head_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
+    constexpr int DS = D / SLICES, LPR = DS / 4;
+    __shared__ Joined joined[WARPS][LPR];
+    grid_dependency_wait();
+    const MergeHead m = merge_head(p, blockIdx.x, cols, sub);
+    if (m.parts == 1) return;       // its warp wrote the result
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.y * DS + (lane % LPR) * 4;
+    Joined r = join_warp<LPR>(join_parts<D, 4>(p, m, cols, threadIdx.x / LPR, 32 * WARPS / LPR, d));
+    if (lane < LPR) joined[warp][lane] = r;
     __syncthreads();
-    float MM = -FLT_MAX, LL = 0.f;
-    for (int i = 0; i < warps; ++i) MM = fmaxf(MM, s_m[i]);
-    for (int i = 0; i < warps; ++i) LL = fmaf(s_l[i], ex2_approx(s_m[i] - MM), LL);
-    if (threadIdx.x < DS) {
-        float v = 0.f;
-        for (int i = 0; i < warps; ++i) v = fmaf(s_o[i][threadIdx.x], ex2_approx(s_m[i] - MM), v);
-        v = LL == 0.f ? 0.f : v / LL;
-        p.out[b * p.out_stride[0] + (int64_t)hq * p.out_stride[1] + blockIdx.y * DS + threadIdx.x] =
-            (uint16_t)((q_bf16 ? pack2<true>(v, 0.f) : pack2<false>(v, 0.f)) & 0xFFFFu);
+    if (threadIdx.x < LPR) {
+        r = joined[0][threadIdx.x];
+        for (int w = 1; w < WARPS; ++w) r = join(r, joined[w][threadIdx.x]);
+        write_joined(p, q_bf16, m, r, d);
     }
-    if (threadIdx.x == 0 && blockIdx.y == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq] = LL == 0.f ? -INFINITY : (MM + log2f(LL)) * kCdLn2;
+}
+
+// Many heads: a warp each; a head of more than kAlone parts is joined by its CTA's eight warps.
+constexpr int kAlone = 32;
+template <int D>
+__global__ void __launch_bounds__(256) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
+    constexpr int LPR = D / 4, GROUPS = 32 / LPR;
+    __shared__ MergeHead heads[8];
+    __shared__ Joined joined[8][LPR];
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = (lane % LPR) * 4;
+    const int64_t i = (int64_t)blockIdx.x * 8 + warp;
+    MergeHead m = {0, 0, 0, 1, 0};
+    if (i < (int64_t)p.B * p.HQ) m = merge_head(p, i, cols, sub);
+    if (m.parts != 1 && m.parts <= kAlone) {
+        const Joined r = join_warp<LPR>(join_parts<D, 8>(p, m, cols, lane / LPR, GROUPS, d));
+        if (lane < LPR) write_joined(p, q_bf16, m, r, d);
+    }
+    if (lane == 0) heads[warp] = m;
+    if (!__syncthreads_or(m.parts > kAlone)) return;
+    for (int w = 0; w < 8; ++w) {
+        m = heads[w];
+        if (m.parts <= kAlone) continue;
+        Joined r = join_warp<LPR>(join_parts<D, 8>(p, m, cols, threadIdx.x / LPR, 8 * GROUPS, d));
+        if (lane < LPR) joined[warp][lane] = r;
+        __syncthreads();
+        if (threadIdx.x < LPR) {
+            r = joined[0][threadIdx.x];
+            for (int k = 1; k < 8; ++k) r = join(r, joined[k][threadIdx.x]);
+            write_joined(p, q_bf16, m, r, d);
+        }
+        __syncthreads();
+    }
 }
 
 constexpr int kMaxOcc = 3;
@@ -774,11 +832,16 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     if ((int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
     e = launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p, q_bf16);
     if (e != cudaSuccess) return e;
-    // The merge: few heads may have many parts each (four CTAs a head), many heads have few.
     const int64_t heads = (int64_t)p.B * p.HQ;
     const int cols = 8 * NT, sub = C::sub;
-    if (heads <= nsm) return launch_early(cache_decode_merge_kernel<D, 4>, dim3((unsigned)heads, 4), dim3(kMergeThreads), 0, st, p, q_bf16, cols, sub);
-    return launch_early(cache_decode_merge_kernel<D, 1>, dim3((unsigned)heads), dim3(128), 0, st, p, q_bf16, cols, sub);
+    // A warp takes 4 or 8 parts (D = 64: twice that) in the time of one load, and a head has
+    // workers / heads of them on average: few heads get four CTAs of 16 warps each, more get four
+    // warps (1024 heads of 14 parts: 30 us with four, 33 with one; 3072 heads of 4: 236 and 232).
+    if (heads <= nsm)
+        return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, q_bf16, cols, sub);
+    if (heads <= 12 * nsm)
+        return launch_early(cache_decode_merge_head_kernel<D, 1, 4>, dim3((unsigned)heads), dim3(128), 0, st, p, q_bf16, cols, sub);
+    return launch_early(cache_decode_merge_kernel<D>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, st, p, q_bf16, cols, sub);
 }
 
 }  // namespace
