@@ -8,6 +8,10 @@
 // computed.  A call returns its outputs, or the library's status as an int when that is not FA_OK.
 #include <Python.h>
 
+#include <algorithm>
+#include <cstdint>
+#include <string>
+
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
@@ -47,6 +51,12 @@ int64_t integer(PyObject* o) {
     const int64_t v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Refused{nullptr, {}};
     return v;
+}
+
+int32_t int32(PyObject* o, const char* name) {
+    const int64_t v = integer(o);
+    if (v < INT32_MIN || v > INT32_MAX) throw Refused{PyExc_ValueError, std::string(name) + " does not fit in 32 bits"};
+    return (int32_t)v;
 }
 
 double number(PyObject* o) {
@@ -89,13 +99,24 @@ Table page_table(PyObject* o, int device, int64_t B) {
     return {t.data_ptr<int32_t>(), B > 1 ? t.stride(0) : t.size(1), t.size(1)};
 }
 
-// The caller's stream, an address, or the device's current one.
-void* stream_of(PyObject* o, int device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
-    void* p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw Refused{nullptr, {}};
-    return p;
-}
+// The device and the stream of a call: the caller's (an address) or the device's current one.  Both
+// are current while it lives, so what is allocated belongs to that stream: memory freed when the
+// call returns goes to no other stream's work while the kernels may still be running.
+struct Place {
+    Place(int device, PyObject* stream) : on(static_cast<c10::DeviceIndex>(device)) {
+        if (stream == Py_None) {
+            at = c10::cuda::getCurrentCUDAStream(on.current_device().index()).stream();
+            return;
+        }
+        at = static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
+        if (!at && PyErr_Occurred()) throw Refused{nullptr, {}};
+        const auto index = on.current_device().index();
+        using_stream.reset_stream(at ? c10::cuda::getStreamFromExternal(at, index) : c10::cuda::getDefaultCUDAStream(index));
+    }
+    c10::cuda::CUDAGuard on;
+    c10::cuda::OptionalCUDAStreamGuard using_stream;
+    cudaStream_t at = nullptr;
+};
 
 const fa_kv_cache_t* cache_at(PyObject* o) {
     const auto* c = static_cast<const fa_kv_cache_t*>(PyLong_AsVoidPtr(o));
@@ -157,7 +178,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
             pos = p.data_ptr<int32_t>();
             pos_stride = rows && dq.B > 1 ? p.stride(0) : 0;
         }
-        const c10::cuda::OptionalCUDAGuard on(q.device());
+        const Place place(device, a[10]);
         const at::Tensor q_out = a[8] == Py_None ? at::empty_like(q) : tensor(a[8], "q_out");
         require(cuda_index(q_out) == device, "q_out must be on q's device");
         dqo = describe(q_out);
@@ -171,8 +192,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
             require(a[9] == Py_None, "k_out without k");
         }
         const fa_status_t s = g_entry.rotary(&dq, has_k ? &dk : nullptr, pos, pos_stride, integer(a[3]), f.data_ptr<double>(),
-                                             (int32_t)(2 * f.numel()), (int32_t)integer(a[5]), (float)number(a[6]),
-                                             (int32_t)integer(a[7]), &dqo, has_k ? &dko : nullptr, stream_of(a[10], device));
+                                             (int32_t)std::min<int64_t>(2 * f.numel(), INT32_MAX), int32(a[5], "layout"),
+                                             (float)number(a[6]), int32(a[7], "inverse"), &dqo, has_k ? &dko : nullptr, place.at);
         return status_or(s, q_out, has_k ? &k_out : nullptr);
     });
 }
@@ -181,15 +202,15 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const fa_kv_cache_t* c = cache_at(a[0]);
-        const int device = (int)integer(a[1]);
+        const int device = int32(a[1], "device");
         const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
         require(cuda_index(k) == device && cuda_index(v) == device, "k and v must be on the cache's device");
         const fa_tensor_t dk = describe(k), dv = describe(v);
         const Table t = page_table(a[4], device, dk.B);
         const int32_t* start = int32_rows(a[5], "start", device, dk.B);
         const int32_t* count = int32_rows(a[6], "count", device, dk.B, true);
-        const c10::cuda::OptionalCUDAGuard on(k.device());
-        const fa_status_t s = g_entry.append(&dk, &dv, c, t.data, t.stride, t.width, start, count, stream_of(a[7], device));
+        const Place place(device, a[7]);
+        const fa_status_t s = g_entry.append(&dk, &dv, c, t.data, t.stride, t.width, start, count, place.at);
         if (s != FA_OK) return PyLong_FromLong(s);
         Py_RETURN_NONE;
     });
@@ -200,7 +221,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 10, [&] {
         const fa_kv_cache_t* c = cache_at(a[0]);
-        const int device = (int)integer(a[1]);
+        const int device = int32(a[1], "device");
         const at::Tensor& table = tensor(a[2], "page_table");
         require(table.dim() == 2, "page_table must be an int32 tensor (B, n) with contiguous rows on the cache's device");
         const int64_t B = table.size(0), S = integer(a[4]);
@@ -208,7 +229,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Table t = page_table(a[2], device, B);
         const int32_t* lens = int32_rows(a[3], "kv_lens", device, B);
         const int32_t* start = int32_rows(a[5], "start", device, B, true);
-        const c10::cuda::OptionalCUDAGuard on(table.device());
+        const Place place(device, a[9]);
         at::Tensor out[2];
         fa_tensor_t d[2];
         for (int i = 0; i < 2; ++i) {
@@ -219,7 +240,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             require(cuda_index(out[i]) == device && d[i].B == B && d[i].H == c->H && d[i].S == S && d[i].D == c->D,
                     "k_out and v_out must be (B, H, S, D) tensors on the cache's device");
         }
-        const fa_status_t s = g_entry.read(c, t.data, t.stride, t.width, start, lens, &d[0], &d[1], stream_of(a[9], device));
+        const fa_status_t s = g_entry.read(c, t.data, t.stride, t.width, start, lens, &d[0], &d[1], place.at);
         return status_or(s, out[0], &out[1]);
     });
 }
@@ -229,13 +250,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 14, [&] {
         const fa_kv_cache_t* c = cache_at(a[0]);
-        const int device = (int)integer(a[1]);
+        const int device = int32(a[1], "device");
         const at::Tensor& q = tensor(a[2], "q");
         require(cuda_index(q) == device, "q must be on the cache's device");
         fa_tensor_t dq = describe(q);
         const Table t = page_table(a[3], device, dq.B);
         const int32_t* lens = int32_rows(a[4], "kv_lens", device, dq.B);
-        const c10::cuda::OptionalCUDAGuard on(q.device());
+        const Place place(device, a[13]);
         const at::Tensor out = a[9] == Py_None ? at::empty_like(q) : tensor(a[9], "out");
         require(cuda_index(out) == device, "out must be on the cache's device");
         fa_tensor_t dout = describe(out);
@@ -256,9 +277,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ws = at::empty({(int64_t)g_entry.decode_bytes(dq.B, dq.H, c->H, dq.D)}, q.options().dtype(at::kByte));
         }
         const fa_status_t s = g_entry.decode(
-            &dq, c, t.data, t.stride, t.width, lens, (int32_t)integer(a[5]), (uint32_t)integer(a[6]),
+            &dq, c, t.data, t.stride, t.width, lens, int32(a[5], "window"), (uint32_t)int32(a[6], "score_mod"),
             a[7] == Py_None ? nullptr : static_cast<const fa_score_params_t*>(PyLong_AsVoidPtr(a[7])), (float)number(a[8]),
-            &dout, lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.nbytes(), stream_of(a[13], device));
+            &dout, lse.defined() ? lse.data_ptr<float>() : nullptr, ws.data_ptr(), (size_t)ws.nbytes(), place.at);
         return status_or(s, out, lse.defined() ? &lse : nullptr);
     });
 }

@@ -174,6 +174,7 @@ __device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int
     const int n = (p.B + 31) / 32;
     const int b0 = min(p.B, lane * n), b1 = min(p.B, b0 + n);
     int64_t mine = 0;
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) mine += seq_range(p, b, sub).steps;
     mine *= p.c.H;
     int64_t before = mine;
@@ -679,10 +680,10 @@ __device__ __forceinline__ Joined join(const Joined& a, const Joined& b) {
 struct MergeHead {
     int b, hq, col, parts, slot;
 };
-__device__ __forceinline__ MergeHead merge_head(const CacheDecodeParams& p, int64_t i, int cols, int sub) {
+__device__ __forceinline__ MergeHead merge_head(const CacheDecodeParams& p, int i, int cols, int sub) {
     MergeHead m;
-    m.b = (int)(i / p.HQ);
-    m.hq = (int)(i - (int64_t)m.b * p.HQ);
+    m.b = i / p.HQ;
+    m.hq = i - m.b * p.HQ;
     const int CB = col_blocks(p.group, cols), h = m.hq / p.group, g = m.hq - h * p.group, cb = g / cols;
     m.col = g - cb * cols;
     const int2 e = p.heads[((int64_t)m.b * p.c.H + h) * CB + cb];      // nobody's, where there are no keys
@@ -770,36 +771,33 @@ __global__ void __launch_bounds__(32 * WARPS) cache_decode_merge_head_kernel(con
     }
 }
 
-// Many heads: a warp each; a head of more than kAlone parts is joined by its CTA's eight warps.
-constexpr int kAlone = 32;
+// A CTA for all the query heads of a (sequence, kv head, block of columns): a thread joins four dims
+// of one of them over every `groups`-th part.
+constexpr int kBlockThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(256) cache_decode_merge_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
-    constexpr int LPR = D / 4, GROUPS = 32 / LPR;
-    __shared__ MergeHead heads[8];
-    __shared__ Joined joined[8][LPR];
+__global__ void __launch_bounds__(kBlockThreads) cache_decode_merge_block_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16, int cols, int sub) {
+    constexpr int LPR = D / 4;
+    __shared__ Joined joined[kBlockThreads];
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = (lane % LPR) * 4;
-    const int64_t i = (int64_t)blockIdx.x * 8 + warp;
-    MergeHead m = {0, 0, 0, 1, 0};
-    if (i < (int64_t)p.B * p.HQ) m = merge_head(p, i, cols, sub);
-    if (m.parts != 1 && m.parts <= kAlone) {
-        const Joined r = join_warp<LPR>(join_parts<D, 8>(p, m, cols, lane / LPR, GROUPS, d));
-        if (lane < LPR) write_joined(p, q_bf16, m, r, d);
-    }
-    if (lane == 0) heads[warp] = m;
-    if (!__syncthreads_or(m.parts > kAlone)) return;
-    for (int w = 0; w < 8; ++w) {
-        m = heads[w];
-        if (m.parts <= kAlone) continue;
-        Joined r = join_warp<LPR>(join_parts<D, 8>(p, m, cols, threadIdx.x / LPR, 8 * GROUPS, d));
-        if (lane < LPR) joined[warp][lane] = r;
-        __syncthreads();
-        if (threadIdx.x < LPR) {
-            r = joined[0][threadIdx.x];
-            for (int k = 1; k < 8; ++k) r = join(r, joined[k][threadIdx.x]);
-            write_joined(p, q_bf16, m, r, d);
+    const int CB = col_blocks(p.group, cols);
+    const int2 e = p.heads[blockIdx.x];
+    const int kv = blockIdx.x / CB, cb = blockIdx.x - kv * CB, b = kv / p.c.H, h = kv - b * p.c.H;
+    const bool none = seq_range(p, b, sub).steps == 0;
+    if (!none && e.x == 1) return;      // its warp wrote the result
+    const int used = min(cols, p.group - cb * cols), items = used * LPR;
+    const int groups = items < kBlockThreads ? kBlockThreads / items : 1;
+    for (int i0 = 0; i0 < items; i0 += kBlockThreads) {
+        const int i = i0 + (groups > 1 ? (int)threadIdx.x % items : (int)threadIdx.x), grp = groups > 1 ? threadIdx.x / items : 0;
+        const int col = i / LPR, d = (i - col * LPR) * 4;
+        const MergeHead m = {b, h * p.group + cb * cols + col, col, none ? 0 : e.x, e.y};
+        Joined r = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (i < items && grp < groups) r = join_parts<D, 4>(p, m, cols, grp, groups, d);
+        if (groups > 1) {
+            joined[threadIdx.x] = r;
+            __syncthreads();
+            for (int k = 1; grp == 0 && k < groups; ++k) r = join(r, joined[k * items + i]);
         }
-        __syncthreads();
+        if (i < items && grp == 0) write_joined(p, q_bf16, m, r, d);
     }
 }
 
@@ -834,14 +832,17 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     if (e != cudaSuccess) return e;
     const int64_t heads = (int64_t)p.B * p.HQ;
     const int cols = 8 * NT, sub = C::sub;
-    // A warp takes 4 or 8 parts (D = 64: twice that) in the time of one load, and a head has
-    // workers / heads of them on average: few heads get four CTAs of 16 warps each, more get four
-    // warps (1024 heads of 14 parts: 30 us with four, 33 with one; 3072 heads of 4: 236 and 232).
+    // The merge.  A head has workers / blocks parts on average, and what counts is how many loads
+    // follow one another and how many CTAs start: few heads get four CTAs of 16 warps each, more get
+    // four warps, and where heads are many, and their parts few, a CTA takes all the query heads of a
+    // kv head (whole calls: 1024 heads of 14 parts 30 us with four warps a head, 33 with one; 5824
+    // heads of one part 7.5 us by kv heads, 11.8 with four warps a query head).
+    const int64_t blocks = (int64_t)p.B * p.c.H * col_blocks(p.group, cols);
     if (heads <= nsm)
         return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, q_bf16, cols, sub);
     if (heads <= 12 * nsm)
         return launch_early(cache_decode_merge_head_kernel<D, 1, 4>, dim3((unsigned)heads), dim3(128), 0, st, p, q_bf16, cols, sub);
-    return launch_early(cache_decode_merge_kernel<D>, dim3((unsigned)((heads + 7) / 8)), dim3(256), 0, st, p, q_bf16, cols, sub);
+    return launch_early(cache_decode_merge_block_kernel<D>, dim3((unsigned)blocks), dim3(kBlockThreads), 0, st, p, q_bf16, cols, sub);
 }
 
 }  // namespace

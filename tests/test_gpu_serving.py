@@ -131,6 +131,8 @@ def test_rotary_refusals():
                 dict(frequencies=f.float()), dict(frequencies=f.cpu()), dict(q=q.cpu()), dict(k=q.cpu())):
         with pytest.raises(ValueError):
             fa.rotary(**{"q": q, "k": None, "positions": i32(0, 1, 2, 3), "frequencies": f, **bad})
+    with pytest.raises(ValueError):
+        fa.rotary(q, None, 0, f, k_out=q)
     for bad in (q.float(), rand((1, 2, 4, 68))[..., :64]):
         with pytest.raises((TypeError, fa.FaError)):
             fa.rotary(bad, None, 0, f)
@@ -398,6 +400,18 @@ def test_decode_score_mods(kind, mod, window):
         check_decode(q, out, lse, K, V, lens, window, 20.0 if mod & 1 else None, s64, 0.2, kind)
 
 
+@pytest.mark.parametrize("B, HQ, H, n, long", [(40, 64, 4, 60, 9000), (300, 12, 1, 40, 0), (3, 96, 2, 700, 0), (30, 2, 2, 30, 20000)])
+def test_decode_many_heads_and_one_long_sequence(B, HQ, H, n, long):
+    # The ways in which the parts of a head are joined: heads of no, one, few and very many parts.
+    fa = fa_module()
+    lens = [(7 * b) % (n + 1) for b in range(B)]
+    lens[B // 2] = long or n
+    cache, table, K, V = random_cache("s8", lens, 16, H, 64, seed=B)
+    q = rand((B, HQ, 1, 64), seed=7, scale=1.5)
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    check_decode(q, out, lse, K, V, lens, kind="s8")
+
+
 @pytest.mark.parametrize("kind, B, HQ, H, n", [("s8", 1, 8, 8, 70001), ("bf16", 1, 32, 2, 40003), ("e4m3", 300, 4, 1, 90),
                                                ("f16", 3, 5, 5, 9000), ("bf16", 700, 2, 2, 1)])
 def test_decode_long_contexts_and_large_batches(kind, B, HQ, H, n):
@@ -527,6 +541,11 @@ def test_decode_strides_streams_and_own_buffers():
     assert (out.as_strided((2, 8, 128), (2048, 256, 1), 128) == 5).all()         # the gap rows
     check_decode(q, out, lse, K, V, lens, kind="e4m3")
     assert fa.decode_attention(q, cache, table, i32(*lens), return_lse=False)[1] is None
+    for s in (side, side.cuda_stream):                   # the stream as an argument
+        side.wait_stream(torch.cuda.current_stream())
+        got, glse = fa.decode_attention(q, cache, table, i32(*lens), stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, base) and torch.equal(glse, blse)
     with pytest.raises(fa.FaError, match="workspace"):
         fa.decode_attention(q, cache, table, i32(*lens), workspace=ws[:8])
 
@@ -537,7 +556,7 @@ def test_decode_refusals():
     q, n = rand((2, 4, 1, 64)), i32(20, 20)
     for bad in (dict(q=q.cpu()), dict(kv_lens=n.long()), dict(kv_lens=n[:1]), dict(kv_lens=n.cpu()),
                 dict(page_table=table[:1]), dict(page_table=table.long()), dict(lse=torch.empty(2, 4, device="cuda")),
-                dict(out=q.cpu())):
+                dict(out=q.cpu()), dict(window=2 ** 32 + 5), dict(workspace=torch.empty(1 << 24, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             fa.decode_attention(**{"q": q, "cache": cache, "page_table": table, "kv_lens": n, **bad})
     for bad in (rand((2, 3, 1, 64)), rand((2, 4, 2, 64)), rand((2, 4, 1, 128))):
@@ -554,6 +573,14 @@ def test_decode_refusals():
         fa.decode_attention(q, c, table, n)
     with pytest.raises(fa.FaError):
         fa.cache_append(make_cache("f16", 2, 2, 16, 64), q[:, :2], q[:, :2], table, i32(0, 0))
+    with pytest.raises(TypeError):
+        fa.cache_read(cache, table, n, 4, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        fa.cache_read(cache, table, n, -1)
+    with pytest.raises(ValueError):
+        fa.cache_append(cache, q[:, :2], q[:, :2].cpu(), table, i32(0, 0))
+    with pytest.raises(ValueError):
+        fa.cache_append(cache, q[:, :2], q[:, :2], table, i32(0, 0), count=i32(1))
     with pytest.raises(ValueError):
         fa.cache_read(cache, table, n, 4, k_out=torch.empty(2, 2, 5, 64, dtype=torch.bfloat16, device="cuda"))
     none = torch.empty(0, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
