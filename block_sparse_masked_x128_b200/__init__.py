@@ -8,6 +8,10 @@ shared library has not been built (``python block_sparse_masked_x128_b200/build.
 Low-level names mirror the C entry points (``fa_create_block_mask``, ``fa_forward``, ...).
 ``create_block_mask`` and ``flex_attention`` are the convenience forms named after the
 FlexAttention API the pages use ("How to Use FlexAttention on Apple Silicon", Setup).
+
+``rotary``, ``PagedKVCache``, ``cache_append``, ``cache_read`` and ``decode_attention`` (serving.py)
+are the forms of fa_rotary, fa_cache_append, fa_cache_read and fa_decode; a decode step makes these
+calls back to back, so their checks and allocations are compiled (``_lib/fa_b200_torch.so``).
 """
 from __future__ import annotations
 

@@ -16,6 +16,10 @@
  *                          Silicon", "The two hooks" and "Bonus: a score_mod for
  *                          soft-capping").
  *
+ * Around them: the backward, the paged forward, the masked softmax, and for serving fa_rotary
+ * (rotary positions), fa_cache_append / fa_cache_read (a paged, possibly 8-bit K/V cache) and
+ * fa_decode (attention of one new token per sequence over it).
+ *
  * Conventions shared by every call:
  *   - All tensor data pointers are DEVICE pointers owned by the caller unless stated.
  *   - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).
@@ -437,6 +441,11 @@ typedef struct fa_kv_cache {
  *   outside [0, table_width * page_size] is skipped (decode: clamped) and recorded:
  *   fa_cache_status then returns FA_ERR_INVALID_ARG.
  *   Two rows of one call must not go to the same place of the cache.
+ *   All of them, and fa_rotary, may be captured into a CUDA graph: what changes from replay to
+ *   replay (positions, lengths, tables, rows) is device data, and nothing is kept between calls.
+ *   Launch each kind of call once before the first capture, so that its kernels are loaded.  The
+ *   kernels are launched to overlap the end of the previous kernel on the stream; each waits for
+ *   that kernel's end before its first read or write.
  *
  * fa_cache_append -- write the new rows k and v (B, H, S, D), fp16 or bf16 (a 16-bit cache's own
  * dtype), of each sequence b at positions start[b] + s for s < count[b] (count NULL: all S rows),
