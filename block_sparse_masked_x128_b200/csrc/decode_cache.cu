@@ -26,11 +26,12 @@
 //   8 bits     codes become fp16 exactly, in registers.  The key's scale multiplies its score, the
 //              value's scale the weight, both in fp32.  q is brought into fp16's range by a power of
 //              two a head, so it keeps all its bits.
-//   Softmax    a head's weights are w_j = 2^(x_j - m) vscale_j, rounded to 16 bits for the product
-//              (the sum of the 2^(x_j - m) is fp32).  The reference m is raised, to the largest
+//   Softmax    a head's weights are w_j = 2^(x_j - m) vscale_j; for the product they become one fp16
+//              number over 8-bit caches, two 16-bit numbers over 16-bit ones (the sum of the
+//              2^(x_j - m) is fp32).  The reference m is raised, to the largest
 //              x_j + log2 vscale_j so far, only when a weight exceeds 2^8: most tiles need no
-//              reduction over the lanes, and a weight is held to 2^-12 of itself or, in fp16, 2^-25
-//              of the largest, however the v scales differ.
+//              reduction over the lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16
+//              at least) or, in fp16, 2^-25 of the largest, however the v scales differ.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -125,6 +126,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return make_float2(__half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))), __half2float(__ushort_as_half((unsigned short)(w >> 16))));
 }
 
 // Bytes 2 HI and 2 HI + 1 of four codes as two fp16 values, exactly.  s8: the code plus 128 in the
@@ -395,8 +402,9 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     const uint32_t w[2] = {raw[s].x, raw[s].y};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        f[s][2 * i] = q_bf16 ? __uint_as_float(w[i] << 16) : __half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)));
-                        f[s][2 * i + 1] = q_bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
+                        const float2 two = q_bf16 ? unpack2<true>(w[i]) : unpack2<false>(w[i]);
+                        f[s][2 * i] = two.x;
+                        f[s][2 * i + 1] = two.y;
                         top = max(top, max(__float_as_uint(f[s][2 * i]) & 0x7fffffffu, __float_as_uint(f[s][2 * i + 1]) & 0x7fffffffu));
                     }
                 }
@@ -558,15 +566,23 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             }
 #pragma unroll
             for (int u = 0; u < C::sub; ++u) {
-                // The weights' transpose is the second operand.
-                uint32_t pb[NT][2];
+                // The weights' transpose is the second operand.  For 16-bit caches, whose products have
+                // time to spare, a weight goes as two numbers, itself rounded and the rest: 8 bits of
+                // it in bf16 alone put the result's error at 1.3 times that of its own rounding.
+                constexpr int PARTS = C::k8 ? 1 : 2;
+                uint32_t pb[PARTS][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         l[nt][0] += e2[u][nt][2 * i];
                         l[nt][1] += e2[u][nt][2 * i + 1];
-                        pb[nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i], w[u][nt][2 * i + 1]));
+                        const uint32_t two = pack2<BF16>(w[u][nt][2 * i], w[u][nt][2 * i + 1]);
+                        pb[0][nt][i] = transpose8x8(two);
+                        if constexpr (!C::k8) {
+                            const float2 r2 = unpack2<BF16>(two);
+                            pb[1][nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i] - r2.x, w[u][nt][2 * i + 1] - r2.y));
+                        }
                     }
                 // O^T += V^T P^T: rows are dims, lane (r, c) holds D / 8 of them for its four keys.
                 const uint32_t vst = st + u * C::tile + C::kbytes;
@@ -591,7 +607,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             const uint32_t a0 = codes_to_half2<DT, 0>(pa), a1 = codes_to_half2<DT, 1>(pa);
                             const uint32_t a2 = codes_to_half2<DT, 0>(pc), a3 = codes_to_half2<DT, 1>(pc);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
                         }
                 } else {
 #pragma unroll
@@ -607,7 +623,9 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             const uint32_t a0 = __byte_perm(v[0][q], v[1][q], 0x5410), a1 = __byte_perm(v[0][q], v[1][q], 0x7632);
                             const uint32_t a2 = __byte_perm(v[2][q], v[3][q], 0x5410), a3 = __byte_perm(v[2][q], v[3][q], 0x7632);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int k = 0; k < PARTS; ++k) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
                         }
                     }
                 }

@@ -338,11 +338,12 @@ def random_cache(kind, lens, page, H, D, seed=0, transposed=False, garbage=True,
 
 
 def check_decode(q, out, lse, K, V, lens, window=0, softcap=None, slopes=None, scale=None, kind="bf16", vscale=None):
-    # The weights are rounded to 16 bits before their product with V (bf16 for a bf16 cache,
-    # fp16 otherwise), scores are fp32 sums of D products, the result is rounded once.  fp16 weights
+    # The weights are rounded before their product with V: over an 8-bit cache to fp16 (2^-11), over
+    # a 16-bit one to a number of its type and another of the rest (the square of its half step);
+    # scores are fp32 sums of D products, the result is rounded once.  fp16 weights
     # (p times the value's scale, the largest at least 1) below 2^-14 are off by up to 2^-25
     # whatever their size: 2^-25 max(p s) |v| / s of each key.
-    step = HALF_STEP[torch.bfloat16 if kind == "bf16" else torch.float16]
+    step = 2.0 ** -11 if kind in ("s8", "e4m3") else HALF_STEP[TYPES[kind]] ** 2
     D = q.shape[3]
     for b, n in enumerate(lens):
         o, l, weight, reach, fine = ref.decode(np64(q[b, :, 0]), K[b], V[b], n, window, softcap, slopes, scale, vscale)
