@@ -32,6 +32,11 @@
 //              x_j + log2 vscale_j so far, only when a weight exceeds 2^8: most tiles need no
 //              reduction over the lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16
 //              at least) or, in fp16, 2^-25 of the largest, however the v scales differ.
+//
+// Measured (whole calls, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k tokens, bf16,
+// D = 128: 75 us, 6.15 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 234 us, 6.4 TB/s;
+// one of 131072 tokens, 32 over 8 heads, e4m3: 52 us, 5.3 TB/s, of them 4 us the merge; one of 257
+// tokens: 6.5 us.  Without its arithmetic the kernel takes 2.4 us less at 8 bits, nothing less at 16.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -72,7 +77,8 @@ struct CdConfig {
     static constexpr int vbytes = 4 * vch * 32 * vb;      // 4 rows a lane
     static constexpr int tile = kbytes + vbytes + (k8 ? 128 : 0);
     // Tiles a warp works on at once: two independent chains of products and half the loop's
-    // overhead, where the ring has room for it.
+    // overhead, where the ring has room for it (131072 tokens of e4m3: 52 us, with one tile 53.3
+    // at three CTAs an SM and 55.3 at four; with two CTAs and deeper rings 53.3).
     static constexpr int sub = D * bytes == 256 ? 1 : 2;
     static constexpr int stage = sub * tile;
     static constexpr int occ = NT == 1 ? 3 : 2;

@@ -31,6 +31,9 @@ fa_status_t cuda_fail(cudaError_t e, const char* what) {
     return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Query heads a kv head: a warp takes 16, and every block of them needs warps of its own.
+constexpr int kMaxGroup = 1024;
+
 // A pointer that the kernels read through, aligned to `align` bytes.
 fa_status_t check_pointer(const void* ptr, size_t align, int dev, const char* name) {
     if ((reinterpret_cast<uintptr_t>(ptr) & (align - 1)) != 0)
@@ -302,7 +305,7 @@ fa_status_t fa_cache_read(const fa_kv_cache_t* cache, const int32_t* page_table,
 }
 
 size_t fa_decode_workspace_bytes(int64_t B, int64_t HQ, int64_t H, int64_t D) {
-    if (B <= 0 || HQ <= 0 || H <= 0 || HQ % H != 0 || B > 65535 || HQ > 65535 || (D != 64 && D != 128)) return 0;
+    if (B <= 0 || HQ <= 0 || H <= 0 || HQ % H != 0 || B > 65535 || HQ > 65535 || HQ / H > kMaxGroup || (D != 64 && D != 128)) return 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
@@ -325,6 +328,8 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     if (q->D != cache->D) return fail(FA_ERR_INVALID_ARG, "q and cache must share D");
     if (q->H % cache->H != 0 || q->H > 65535)
         return fail(FA_ERR_INVALID_ARG, "%lld query heads are no multiple of %lld kv heads", (long long)q->H, (long long)cache->H);
+    if (q->H / cache->H > kMaxGroup || q->B * q->H > 0x7fffffffLL)
+        return fail(FA_ERR_UNSUPPORTED, "more than %d query heads a kv head, or 2^31 - 1 heads in all", kMaxGroup);
     if (!eight_bit(cache->dtype) && q->dtype != cache->dtype)
         return fail(FA_ERR_INVALID_ARG, "a 16-bit cache takes queries of its own dtype");
     if (window < 0) return fail(FA_ERR_INVALID_ARG, "window must not be negative");

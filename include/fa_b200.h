@@ -469,7 +469,7 @@ fa_status_t fa_cache_read(const fa_kv_cache_t* cache, const int32_t* page_table,
  * fa_decode -- attention of one new token a sequence over a paged cache, heads in groups.
  *
  *   q           (B, HQ, 1, D), fp16 or bf16 (a 16-bit cache's own dtype); HQ a multiple of the
- *               cache's H: query head h reads kv head h / (HQ / H)
+ *               cache's H, at most 1024 times it: query head h reads kv head h / (HQ / H)
  *   kv_lens     device int32 [B]: the tokens of each sequence in the cache, the new one among
  *               them; the query is at position kv_lens[b] - 1.  Read by the kernels, so one
  *               captured call serves every length

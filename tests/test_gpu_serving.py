@@ -401,7 +401,8 @@ def test_decode_score_mods(kind, mod, window):
         check_decode(q, out, lse, K, V, lens, window, 20.0 if mod & 1 else None, s64, 0.2, kind)
 
 
-@pytest.mark.parametrize("B, HQ, H, n, long", [(40, 64, 4, 60, 9000), (300, 12, 1, 40, 0), (3, 96, 2, 700, 0), (30, 2, 2, 30, 20000)])
+@pytest.mark.parametrize("B, HQ, H, n, long", [(40, 64, 4, 60, 9000), (300, 12, 1, 40, 0), (3, 96, 2, 700, 0), (30, 2, 2, 30, 20000),
+                                                  (2, 1024, 1, 500, 0)])
 def test_decode_many_heads_and_one_long_sequence(B, HQ, H, n, long):
     # The ways in which the parts of a head are joined: heads of no, one, few and very many parts.
     fa = fa_module()

@@ -80,6 +80,9 @@ def test_decode_refuses_bad_arguments(fa):
     assert _decode(fa, q, _cache(fa, dtype=0), q) == bad
     big = _t(fa, B=65536, H=4, S=1, D=64)
     assert _decode(fa, big, c, big) == fa.FA_ERR_UNSUPPORTED
+    many = _t(fa, B=1, H=1025, S=1, D=64)
+    assert _decode(fa, many, _cache(fa, H=1), many) == fa.FA_ERR_UNSUPPORTED
+    assert fa.decode_workspace_bytes(1, 1025, 1, 64) == 0
     assert fa.decode_workspace_bytes(0, 4, 2, 64) == 0 and fa.decode_workspace_bytes(1, 3, 2, 64) == 0
 
 
