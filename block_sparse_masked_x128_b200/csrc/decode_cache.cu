@@ -40,6 +40,8 @@
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
+#include <algorithm>
+#include <atomic>
 #include <cfloat>
 
 #include <cuda_fp16.h>
@@ -85,6 +87,8 @@ struct CdConfig {
     static constexpr int stages = (D * bytes == 64 ? 4 : 2) + (NT == 1 ? 0 : 1);
     static constexpr int smem = kCdWarps * stages * stage;
     static constexpr int seg = k8 && D == 128 ? 16 : 8;   // a lane's dims come in runs of this
+    static constexpr int orow = D + D / seg * 4;
+    static_assert(8 * NT * (kCdWarps * (orow + 2) + 2) * 4 <= smem, "join_and_write uses the rings' memory");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {
@@ -228,7 +232,83 @@ __device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int
 // The head groups of a kv head: columns of the products, `rows` of them at a time.
 __host__ __device__ constexpr int col_blocks(int group, int cols) { return (group + cols - 1) / cols; }
 
+// Dims 2k .. 2k + 3 of lane (r, c)'s: contiguous within a run of `seg`.
+template <int SEG>
+__device__ __forceinline__ int lane_dim(int r, int k) {
+    return 2 * k / SEG * 64 + r * SEG + 2 * k % SEG;
+}
+
+// Joins the (m, l, O) of the CTA's warps in shared memory (over the rings, which are done with) and
+// writes the result.
 template <int DT, int D, int NT>
+__device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8_t* smem, const float (&o)[NT][D / 16][4], const float (&m)[NT][2],
+                                               const float (&l)[NT][2], int b, int hq0, int cols, bool q_bf16) {
+    using C = CdConfig<DT, D, NT>;
+    constexpr int COLS = 8 * NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+    float* so = reinterpret_cast<float*>(smem);     // [warp][column] rows of D floats, 4 more after each run (bank conflicts)
+    float* sm = so + kCdWarps * COLS * C::orow;     // [warp][column] m, then the factor of O
+    float* sl = sm + kCdWarps * COLS;               // [warp][column] l
+    float* sM = sl + kCdWarps * COLS;               // [column] M, L
+    float* sL = sM + COLS;
+    cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = nt * 8 + 2 * c + j;
+            float sum = l[nt][j];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
+            if (r == 0) {
+                sm[warp * COLS + col] = m[nt][j];
+                sl[warp * COLS + col] = sum;
+            }
+            float* row = so + (warp * COLS + col) * C::orow;
+#pragma unroll
+            for (int k = 0; k < D / 16; k += 2) {
+                const int dim = lane_dim<C::seg>(r, k);
+                *reinterpret_cast<float4*>(row + dim + dim / C::seg * 4) = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+            }
+        }
+    __syncthreads();
+    if (threadIdx.x < COLS) {
+        const int col = threadIdx.x;
+        float M = -FLT_MAX, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, sm[w * COLS + col]);
+#pragma unroll
+        for (int w = 0; w < kCdWarps; ++w) {
+            const float f = ex2_approx(sm[w * COLS + col] - M);
+            L = fmaf(sl[w * COLS + col], f, L);
+            sm[w * COLS + col] = f;
+        }
+        sM[col] = M;
+        sL[col] = L;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < cols * (D / 4); i += kCdThreads) {
+        const int col = i / (D / 4), dim = (i % (D / 4)) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kCdWarps; ++w) {
+            const float f = sm[w * COLS + col];
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * COLS + col) * C::orow + dim + dim / C::seg * 4);
+            s = make_float4(fmaf(v.x, f, s.x), fmaf(v.y, f, s.y), fmaf(v.z, f, s.z), fmaf(v.w, f, s.w));
+        }
+        const float L = sL[col], inv = L == 0.f ? 0.f : 1.f / L;
+        uint2 w = q_bf16 ? make_uint2(pack2<true>(s.x * inv, s.y * inv), pack2<true>(s.z * inv, s.w * inv))
+                         : make_uint2(pack2<false>(s.x * inv, s.y * inv), pack2<false>(s.z * inv, s.w * inv));
+        if (L == 0.f) w = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1] + dim) = w;
+        if (dim == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = L == 0.f ? -INFINITY : (sM[col] + log2f(L)) * kCdLn2;
+    }
+}
+
+// WHOLE: a CTA takes all the keys of a (sequence, kv head, block of columns), its warps every fourth
+// step, and joins its warps' parts itself: one launch, for tables that map few tokens.
+template <int DT, int D, int NT, bool WHOLE>
 __global__ void __launch_bounds__(kCdThreads, CdConfig<DT, D, NT>::occ)
 cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     using C = CdConfig<DT, D, NT>;
@@ -239,13 +319,27 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
 
     grid_dependency_wait();
-    // With more query heads than columns, neighbouring warps take the same run for one block of
-    // columns each, so the keys are read from HBM once.
     const int CB = col_blocks(p.group, COLS);
-    const int worker = blockIdx.x * kCdWarps + warp;
-    const int mine = worker / CB, cb = worker - mine * CB;
-    const Run run = find_run(p, C::sub, mine, (int)(gridDim.x * kCdWarps) / CB);
-    if (run.seq < 0) return;
+    int worker = 0, mine = 0, cb;
+    Run run;
+    if constexpr (WHOLE) {
+        const int kv = blockIdx.x / CB;
+        cb = blockIdx.x - kv * CB;
+        run.seq = kv / p.c.H;
+        run.head = kv - run.seq * p.c.H;
+        run.step = warp;
+        run.first = 0;
+        run.last = max(0, (seq_range(p, run.seq, C::sub).steps - warp + kCdWarps - 1) / kCdWarps);
+    } else {
+        // With more query heads than columns, neighbouring warps take the same run for one block of
+        // columns each, so the keys are read from HBM once.
+        worker = blockIdx.x * kCdWarps + warp;
+        mine = worker / CB;
+        cb = worker - mine * CB;
+        run = find_run(p, C::sub, mine, (int)(gridDim.x * kCdWarps) / CB);
+        if (run.seq < 0) return;
+    }
+    constexpr int kTiles = WHOLE ? kCdWarps * C::sub : C::sub;      // from a warp's step to its next
     const int col0 = cb * COLS, cols = min(COLS, p.group - col0);
 
     const uint32_t ring = smem_u32(smem) + warp * C::stages * C::stage;
@@ -293,7 +387,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     ld.h = run.head;
     ld.sr = seq_range(p, ld.b, C::sub);
     ld.tile = ld.sr.tile + run.step * C::sub;
-    ld.left = ld.sr.steps - run.step;
+    ld.left = WHOLE ? (int)run.last : ld.sr.steps - run.step;
     ld.todo = run.last - run.first;
     int page[C::sub];                   // looked up one step ahead of their use
     auto look_up = [&]() {
@@ -350,7 +444,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
             for (int u = 0; u < C::sub; ++u)
                 issue_tile(ring + slot * C::stage + u * C::tile, ld.tile + u, page[u], 1u << (slot * C::sub + u));
-            ld.tile += C::sub;
+            ld.tile += kTiles;
             if (--ld.todo > 0) {
                 if (--ld.left > 0) {
                     look_up();
@@ -372,9 +466,10 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 
     int b = run.seq, h = run.head, step0 = run.step, slot = 0;
     SeqRange sr = seq_range(p, b, C::sub);
-    for (int64_t at = run.first; at < run.last;) {
-        // This warp's part of the head: steps step0 .. step0 + steps - 1.
-        const int steps = (int)min((int64_t)(sr.steps - step0), run.last - at);
+    int64_t at = run.first;
+    do {
+        // This warp's part of the head: `steps` of its steps, from step0.
+        const int steps = WHOLE ? (int)run.last : (int)min((int64_t)(sr.steps - step0), run.last - at);
         const int hq0 = h * p.group + col0;
         const bool complete = steps == sr.steps;
 
@@ -445,7 +540,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             for (int t = 0; t < KS; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
         }
         int t = sr.tile + step0 * C::sub;       // first tile of the step at hand
-        for (int i = 0; i < steps; ++i, t += C::sub) {
+        for (int i = 0; i < steps; ++i, t += kTiles) {
             cp_async_wait<C::stages - 2>();
             __syncwarp();       // other lanes' copies have landed too; and all lanes are done with the last slot
             issue(slot == 0 ? C::stages - 1 : slot - 1);
@@ -638,6 +733,10 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             }
             slot = slot + 1 == C::stages ? 0 : slot + 1;
         }
+        if constexpr (WHOLE) {
+            join_and_write<DT, D, NT>(p, smem, o, m, l, b, hq0, cols, q_bf16);
+            return;
+        }
         // The part's (m, l, O), or the result.  A worker's first head has slot 2 worker, a later one
         // that it leaves unfinished slot 2 worker + 1.
         const int part = 2 * worker + (at == run.first ? 0 : 1);
@@ -654,8 +753,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
                 if (col >= cols) continue;
-                // dims 2k .. 2k + 3 of this lane's: contiguous within a run of C::seg
-                auto dim = [&](int k) { return 2 * k / C::seg * 64 + r * C::seg + 2 * k % C::seg; };
+                auto dim = [&](int k) { return lane_dim<C::seg>(r, k); };
                 if (!complete) {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2)
@@ -681,7 +779,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             h = 0;
             do sr = seq_range(p, ++b, C::sub); while (sr.steps == 0);
         }
-    }
+    } while (at < run.last);
     cp_async_wait<0>();
     grid_dependency_release();
 }
@@ -834,25 +932,39 @@ int64_t heads_bytes(int64_t B, int64_t HQ, int64_t HK) {
     return (B * HK * col_blocks(group, columns(group)) * 8 + 15) / 16 * 16;
 }
 
-template <int DT, int D, int NT>
-cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t st) {
+// The kernel, with its shared memory allowed once a device.
+template <int DT, int D, int NT, bool WHOLE>
+cudaError_t launch_kernel(const CacheDecodeParams& p, bool q_bf16, unsigned grid, cudaStream_t st) {
     using C = CdConfig<DT, D, NT>;
-    static_assert(C::occ <= kMaxOcc, "the workspace counts kMaxOcc CTAs an SM");
-    auto kern = cache_decode_kernel<DT, D, NT>;
-    cudaError_t e = cudaSuccess;
-    static std::atomic<uint64_t> ready{0};      // devices on which the kernel may have its shared memory
+    auto kern = cache_decode_kernel<DT, D, NT, WHOLE>;
+    static std::atomic<uint64_t> ready{0};
     int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
+    return launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p, q_bf16);
+}
+
+template <int DT, int D, int NT>
+cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t st) {
+    using C = CdConfig<DT, D, NT>;
+    static_assert(C::occ <= kMaxOcc, "the workspace counts kMaxOcc CTAs an SM");
+    const int64_t blocks = (int64_t)p.B * p.c.H * col_blocks(p.group, 8 * NT);
+    // Where the tables (or the window) leave few keys a head, a CTA each is faster than splitting and
+    // merging: up to 512 keys (8 sequences of 100-200 tokens, 32 over 8 heads: 4.8 us against 8.0; one
+    // of 500, 8 heads: 7.0 against 6.3, with a launch less), and up to 1024 where there is a head for
+    // every SM (32 of 500-1000: 20 against 23; with 16 heads in all 14.8 against 11.5).
+    const int keys = p.window > 0 ? std::min(p.window, p.c.capacity) : p.c.capacity;
+    if (keys <= 512 || (keys <= 1024 && blocks >= nsm))
+        return launch_kernel<DT, D, NT, true>(p, q_bf16, (unsigned)blocks, st);
+    const int grid = nsm * C::occ;
     p.heads = static_cast<int2*>(p.workspace);
     p.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + heads_bytes(p.B, p.HQ, p.c.H));
-    const int grid = nsm * C::occ;
-    if ((int64_t)p.B * p.HQ > 0x7fffffffLL) return cudaErrorInvalidValue;
-    e = launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p, q_bf16);
+    cudaError_t e = launch_kernel<DT, D, NT, false>(p, q_bf16, (unsigned)grid, st);
     if (e != cudaSuccess) return e;
     const int64_t heads = (int64_t)p.B * p.HQ;
     const int cols = 8 * NT, sub = C::sub;
@@ -861,7 +973,6 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     // four warps, and where heads are many, and their parts few, a CTA takes all the query heads of a
     // kv head (whole calls: 1024 heads of 14 parts 30 us with four warps a head, 33 with one; 5824
     // heads of one part 7.5 us by kv heads, 11.8 with four warps a query head).
-    const int64_t blocks = (int64_t)p.B * p.c.H * col_blocks(p.group, cols);
     if (heads <= nsm)
         return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, q_bf16, cols, sub);
     if (heads <= 12 * nsm)

@@ -385,6 +385,24 @@ def test_decode(case, window):
     assert torch.equal(raw(again), raw(out)) and torch.equal(lse, lse2)          # the same bits
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "s8", "e4m3"])
+@pytest.mark.parametrize("B, group, top", [(1, 3, 512), (5, 16, 500), (60, 5, 1024), (3, 2, 1024), (40, 20, 900)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_over_small_tables(kind, B, group, top, D):
+    # Tables that map few tokens: a CTA takes a head's keys alone, or (few heads) they are split.
+    fa = fa_module()
+    lens = [(top - 17 * b) % (top + 1) for b in range(B)]
+    if B > 2:
+        lens[1], lens[2] = 0, 1
+    cache, table, K, V = random_cache(kind, lens, 32, 3, D, seed=B)
+    table = table[:, :-1].contiguous()
+    q = rand((B, 3 * group, 1, D), TYPES["f16" if kind == "f16" else "bf16"], 4, 1.5)
+    for window in (0, 40):
+        out, lse = fa.decode_attention(q, cache, table, i32(*lens), window=window)
+        check_decode(q, out, lse, K, V, lens, window, kind=kind)
+    assert fa.cache_status() == fa.FA_OK
+
+
 @pytest.mark.parametrize("kind", ["bf16", "s8"])
 @pytest.mark.parametrize("mod", [1, 2, 3])
 @pytest.mark.parametrize("window", [0, 70])
