@@ -379,7 +379,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     struct {
         int b, h, tile, left;           // steps left of its head
         SeqRange sr;
-        int64_t todo;                   // steps left of the run
+        int32_t todo;                   // steps left of the run
         int64_t head_off, scale_off;    // the head's offset in a page
         const int32_t* table;
     } ld;
@@ -388,7 +388,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
     ld.sr = seq_range(p, ld.b, C::sub);
     ld.tile = ld.sr.tile + run.step * C::sub;
     ld.left = WHOLE ? (int)run.last : ld.sr.steps - run.step;
-    ld.todo = run.last - run.first;
+    ld.todo = (int)(run.last - run.first);
     int page[C::sub];                   // looked up one step ahead of their use
     auto look_up = [&]() {
 #pragma unroll

@@ -12,10 +12,11 @@
 //
 // Reading moves its bytes once and is bound by HBM (16 sequences of 1k-8k tokens, 16 heads, s8 to
 // bf16: 201 us for 1.31 GB, 0.99 of the copy rate).  Appending is bound by its instructions as much
-// (15k tokens of 8 heads to e4m3: 23 us for 95 MB; 16-bit magnitudes compared two at a time and
-// 32-bit positions halved them).  A row belongs to D / 8 lanes, 16 bytes of 16-bit values each, so
-// its maximum is three or four shuffles and nothing is staged; rows of k and v at the same place go
-// together, two of each in flight (four were slower: 52.7 us against 49.6 for both calls).
+// (15k tokens of 8 heads to e4m3: 19 us for 95 MB; 16-bit magnitudes compared two at a time, 32-bit
+// positions and eight lanes a row took two thirds of them away).  A row belongs to eight or D / 8
+// lanes, so its maximum is a few shuffles and nothing is staged; rows of k and v at the same place go
+// together.  The read has two rows of each in flight (four: 52.7 us against 49.6 for a prompt's write
+// and read).
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -29,7 +30,7 @@ namespace {
 __device__ int32_t g_cache_rows_status;   // 2: a page or position out of range was met
 
 constexpr int kRowThreads = 128;
-constexpr int kRowsAhead = 2;         // rows of k and of v a lane group has in flight
+constexpr int kReadAhead = 2;         // rows of k and of v that a lane group of the read has in flight
 
 template <bool BF16>
 __device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
@@ -105,79 +106,83 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
 }
 
 // The bits, as fp32, of the largest magnitude of a row whose 16-bit values are spread over LPR
-// lanes, eight each: magnitudes order as their bits, two at a time.
-template <bool BF16, int LPR>
-__device__ __forceinline__ uint32_t row_amax(const uint4& r) {
-    uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+// lanes: magnitudes order as their bits, two at a time.
+template <bool BF16, int P, int LPR>
+__device__ __forceinline__ uint32_t row_amax(const uint4 (&r)[P]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(r[i].x & 0x7FFF7FFFu, r[i].y & 0x7FFF7FFFu), __vmaxu2(r[i].z & 0x7FFF7FFFu, r[i].w & 0x7FFF7FFFu)));
 #pragma unroll
     for (int off = LPR / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, off));
     const uint32_t top = max(m & 0xFFFFu, m >> 16);
     return BF16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
 }
 
-// The code bytes of a row's eight values and its scale; `amax` holds the bits of its largest
-// magnitude.
+// What multiplies a row's values: the inverse of its scale, exactly for e4m3 (a power of two),
+// within 2^-22 for s8.
 template <int DT>
-__device__ __forceinline__ uint2 quantise_row(const float (&x)[8], uint32_t amax, float& scale) {
-    scale = row_scale<DT>(amax);
-    if (amax >= 0x7f800000u) return make_uint2(0u, 0u);
-    if constexpr (DT == FA_DTYPE_S8) return quantise_s8x8(x, scale, __fdividef(1.f, scale));
-    const float inv = __uint_as_float(0x7f000000u - __float_as_uint(scale));       // exact: a power of two
+__device__ __forceinline__ float row_inverse(float scale) {
+    if constexpr (DT == FA_DTYPE_E4M3) return __uint_as_float(0x7f000000u - __float_as_uint(scale));
+    return __fdividef(1.f, scale);
+}
+
+// The code bytes of eight of a row's values.
+template <int DT>
+__device__ __forceinline__ uint2 quantise_8(const float (&x)[8], float scale, float inv) {
+    if constexpr (DT == FA_DTYPE_S8) return quantise_s8x8(x, scale, inv);
     return make_uint2(quantise_e4m3x2(x[0] * inv, x[1] * inv) | quantise_e4m3x2(x[2] * inv, x[3] * inv) << 16,
                       quantise_e4m3x2(x[4] * inv, x[5] * inv) | quantise_e4m3x2(x[6] * inv, x[7] * inv) << 16);
 }
 
-// Grid (ceil(S / (groups kRowsAhead)), H, B): a group of D / 8 lanes takes kRowsAhead rows, all
-// loaded before the first is worked on.
-template <int DT, int D, bool BF16>
+// Grid (ceil(S / groups), H, B): LPR lanes take a row of k and of v, D / 8 / LPR pieces of 16 bytes a
+// lane.  Eight lanes a row share its maximum and scale over most values (a prompt's write and read 45.9 us
+// with eight, 49.3 with sixteen); for single rows D / 8 lanes are a little sooner done.
+template <int DT, int D, bool BF16, int LPR>
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_constant__ CacheRowsParams p) {
-    constexpr int LPR = D / 8;
+    constexpr int P = D / 8 / LPR;
     const int RPC = blockDim.x / LPR;
     grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
-    const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
+    const int s = blockIdx.x * RPC + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
     const int count = p.limit ? min(__ldg(p.limit + b), p.S) : p.S;
-    if ((int)(blockIdx.x * RPC * kRowsAhead) >= count) return;
+    if ((int)(blockIdx.x * RPC) >= count) return;
     // A position start + s, as 32 bits without sign: past the capacity where it is negative.
-    const uint32_t start = __ldg(p.start + b);
-    const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
-    uint4 raw[kRowsAhead][2];
-    int page[kRowsAhead];
+    const uint32_t pos = (uint32_t)__ldg(p.start + b) + s;
+    uint4 raw[2][P];
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
-        const int s = s0 + i * RPC;
-        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-        page[i] = -1;
-        if (s < count) {
+    for (int w = 0; w < 2; ++w) {
+        const uint16_t* in = p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8;
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                raw[i][w] = *reinterpret_cast<const uint4*>(p.in[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8);
-            page[i] = cache_page(p.c, table, start + s);
-            if (page[i] < 0) g_cache_rows_status = 2;
-        }
+        for (int k = 0; k < P; ++k) raw[w][k] = s < count ? *reinterpret_cast<const uint4*>(in + 8 * LPR * k) : make_uint4(0, 0, 0, 0);
     }
+    int page = -1;
+    if (s < count) {
+        page = cache_page(p.c, p.c.table + (int64_t)b * p.c.table_stride, pos);
+        if (page < 0) g_cache_rows_status = 2;
+    }
+    const int row = pos & ((1 << p.c.page_shift) - 1);
+    const int64_t at = (int64_t)page * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
+    const int64_t sat = (int64_t)page * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
-        if (!__any_sync(kFullMask, page[i] >= 0)) continue;
-        const int row = (start + s0 + i * RPC) & ((1 << p.c.page_shift) - 1);
-        const int64_t at = (int64_t)page[i] * p.c.stride[0] + h * p.c.stride[1] + (int64_t)row * p.c.stride[2] + sub * 8;
-        const int64_t sat = (int64_t)page[i] * p.c.scale_stride[0] + h * p.c.scale_stride[1] + (int64_t)row * p.c.scale_stride[2];
+    for (int w = 0; w < 2; ++w) {
+        void* pool = w ? p.c.v : p.c.k;
+        if constexpr (!CacheType<DT>::k8) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            void* pool = w ? p.c.v : p.c.k;
-            if constexpr (!CacheType<DT>::k8) {
-                if (page[i] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at) = raw[i][w];
-            } else {
+            for (int k = 0; k < P; ++k)
+                if (page >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + at + 8 * LPR * k) = raw[w][k];
+        } else {
+            const uint32_t amax = row_amax<BF16, P, LPR>(raw[w]);
+            const float scale = row_scale<DT>(amax), inv = row_inverse<DT>(scale);
+            if (page >= 0 && sub == 0) (w ? p.c.v_scale : p.c.k_scale)[sat] = scale;
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
                 float x[8];
-                row_unpack<BF16>(raw[i][w], x);
-                const uint32_t m = row_amax<BF16, LPR>(raw[i][w]);
-                float scale;
-                const uint2 c = quantise_row<DT>(x, m, scale);
-                if (page[i] >= 0) {
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) = c;
-                    if (sub == 0) (w ? p.c.v_scale : p.c.k_scale)[sat] = scale;
-                }
+                row_unpack<BF16>(raw[w][k], x);
+                uint2 c = quantise_8<DT>(x, scale, inv);
+                if (amax >= 0x7f800000u) c = make_uint2(0u, 0u);
+                if (page >= 0) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at + 8 * LPR * k) = c;
             }
         }
     }
@@ -190,15 +195,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
     const int RPC = blockDim.x / LPR;
     grid_dependency_wait();
     const int sub = threadIdx.x % LPR;
-    const int s0 = blockIdx.x * RPC * kRowsAhead + threadIdx.x / LPR;
+    const int s0 = blockIdx.x * RPC * kReadAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
     const uint32_t start = p.start ? __ldg(p.start + b) : 0;
     const int len = __ldg(p.limit + b);
     const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
-    uint4 raw[kRowsAhead][2];
-    float scale[kRowsAhead][2];
+    uint4 raw[kReadAhead][2];
+    float scale[kReadAhead][2];
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
+    for (int i = 0; i < kReadAhead; ++i) {
         const uint32_t pos = start + s0 + i * RPC;      // as in the append
         int page = -1;
         if (s0 + i * RPC < p.S && (int)pos >= 0 && (int)pos < len) {
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
         }
     }
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i) {
+    for (int i = 0; i < kReadAhead; ++i) {
         const int s = s0 + i * RPC;
         if (s >= p.S) continue;
 #pragma unroll
@@ -250,12 +255,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
 
 template <int DT, int D, bool BF16>
 cudaError_t launch_rows(const CacheRowsParams& p, bool append, cudaStream_t st) {
+    const bool few = !append || p.S < 16;
+    const int lanes = few ? D / 8 : 8;
     // A warp is enough for a step's single rows; a block's other warps would only be in the way.
-    const int warps = (int)std::min<int64_t>(kRowThreads / 32, ((int64_t)p.S * (D / 8) + 31) / 32);
-    const int rows = warps * 32 / (D / 8) * kRowsAhead;
+    const int warps = (int)std::min<int64_t>(kRowThreads / 32, ((int64_t)p.S * lanes + 31) / 32);
+    const int rows = warps * 32 / lanes * (append ? 1 : kReadAhead);
     const dim3 grid((unsigned)((p.S + rows - 1) / rows), (unsigned)p.c.H, (unsigned)p.B), block(warps * 32);
-    return append ? launch_early(cache_append_kernel<DT, D, BF16>, grid, block, 0, st, p)
-                  : launch_early(cache_read_kernel<DT, D, BF16>, grid, block, 0, st, p);
+    if (!append) return launch_early(cache_read_kernel<DT, D, BF16>, grid, block, 0, st, p);
+    return few ? launch_early(cache_append_kernel<DT, D, BF16, D / 8>, grid, block, 0, st, p)
+               : launch_early(cache_append_kernel<DT, D, BF16, 8>, grid, block, 0, st, p);
 }
 
 cudaError_t launch_any(const CacheRowsParams& p, int dtype, int D, bool bf16, bool append, cudaStream_t st) {
