@@ -11,9 +11,10 @@
 // it turned, 119 us, 5.65 TB/s or 0.86 of the copy rate; 32 heads x 8192 tokens of D = 64, 14.3 us
 // with the launch.  A CTA takes a few tokens of every head: their cos and sin are computed once into
 // shared memory and serve all heads of q and k.  Work goes in columns of 16 bytes (half layout: the
-// two columns of eight pairs): a thread keeps its column and walks the rows (token, head) by fixed
-// offsets, with the loads of kAhead rows in flight (twice as many: 20.5 us at 8192 tokens).  Pairs
-// that do not fill such columns (half layout with rot_dim no multiple of 16) go one by one.
+// two columns of eight pairs; of 8 bytes where rot_dim is a multiple of 8 but not of 16): a thread
+// keeps its column and walks the rows (token, head) by fixed offsets, with the loads of kAhead rows
+// in flight (twice as many: 20.5 us at 8192 tokens).  Pairs that do not fill such columns (half
+// layout with rot_dim no multiple of 8) go one by one.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -47,17 +48,6 @@ __device__ __forceinline__ uint16_t rot_round(float v) {
     return (uint16_t)(pack2<BF16>(v, 0.f) & 0xFFFFu);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void rot_unpack8(const uint4& r, float (&f)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = rot_unpack<BF16>(w[i]);
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
-}
-
 // cos and sin (times the factor) of the first `half` pairs of tokens t0 .. t0 + nt - 1 of sequence
 // b, pair j of token t at cs[t * pitch + place(j)].
 template <class Place>
@@ -84,26 +74,44 @@ __device__ __forceinline__ RotTile rot_tile(const RotaryParams& p) {
     return r;
 }
 
-// By columns: half layout with rot_dim a multiple of 16, or interleaved with any rot_dim.
-template <bool BF16, bool INTER>
+// W words as one access.
+template <int W>
+__device__ __forceinline__ void load_words(const uint16_t* x, uint32_t (&w)[W]) {
+    if constexpr (W == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(x);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+template <int W>
+__device__ __forceinline__ void store_words(uint16_t* y, const uint32_t (&w)[W]) {
+    if constexpr (W == 4) *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
+}
+
+// By columns of 2 W elements: half layout with rot_dim a multiple of 4 W, or interleaved (W = 4) with
+// any rot_dim.
+template <bool BF16, bool INTER, int W>
 __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __grid_constant__ RotaryParams p) {
     __shared__ __align__(16) float2 cs[kRotTable];
-    constexpr int kAhead = INTER ? 4 : 2;          // rows whose 16-byte loads are in flight at once
-    constexpr int J = INTER ? 4 : 8;               // pairs a column
+    constexpr int kAhead = INTER || W == 2 ? 4 : 2;     // rows whose loads are in flight at once
+    constexpr int E = 2 * W, J = INTER ? W : E;         // elements and pairs a column
     grid_dependency_wait();
     const RotTile tile = rot_tile(p);
     // The columns of a row: rotated ones (half layout: pairs of columns), then copied ones.
     const int rot_cols = (p.half + J - 1) / J;
-    const int copied0 = INTER ? rot_cols * 8 : 2 * p.half;
-    const int cols = rot_cols + (p.in_place ? 0 : (p.D - copied0) / 8);
-    const int col = threadIdx.x % cols, first = threadIdx.x / cols, stride = kRotThreads / cols;   // D <= 1024: cols <= 128
+    const int copied0 = INTER ? rot_cols * E : 2 * p.half;
+    const int cols = rot_cols + (p.in_place ? 0 : (p.D - copied0) / E);
+    const int col = threadIdx.x % cols, first = threadIdx.x / cols, stride = kRotThreads / cols;   // D <= 1024: cols <= 256
     // Two pairs of all columns stand together: neighbouring columns read neighbouring 16 bytes.
     const int pitch = rot_cols * J;
     rot_table(p, cs, tile.b, tile.t0, tile.nt, pitch, [&](int j) { return (j % J / 2) * rot_cols * 2 + j / J * 2 + (j & 1); });
     __syncthreads();
     if (first >= stride) return;
-    const bool turns = col < rot_cols, full = !INTER || col * 4 + 4 <= p.half;
-    const int at = turns ? col * 8 : copied0 + (col - rot_cols) * 8;
+    const bool turns = col < rot_cols, full = !INTER || col * W + W <= p.half;
+    const int at = turns ? col * E : copied0 + (col - rot_cols) * E;
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {                  // q, k
         const int hb = w ? p.H[0] : 0;
@@ -122,14 +130,14 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
         const int64_t x_step = in_step * xi + out_step * xo, x_wrap = xo - inner * xi;
         const int64_t y_step = in_step * yi + out_step * yo, y_wrap = yo - inner * yi;
         for (int rw = first; rw < rows; rw += stride * kAhead) {
-            uint4 a[kAhead], b[kAhead];
+            uint32_t a[kAhead][W], b[kAhead][W];
             int token[kAhead];
             uint16_t* to[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (rw + k * stride < rows) {
-                    a[k] = *reinterpret_cast<const uint4*>(x);
-                    if (!INTER && turns) b[k] = *reinterpret_cast<const uint4*>(x + p.half);
+                    load_words<W>(x, a[k]);
+                    if (!INTER && turns) load_words<W>(x + p.half, b[k]);
                 }
                 token[k] = tok_in ? in : out;
                 to[k] = y;
@@ -147,35 +155,26 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (rw + k * stride >= rows) break;
-                if (!turns) {
-                    *reinterpret_cast<uint4*>(to[k]) = a[k];
-                    continue;
-                }
                 const float2* v = cs + token[k] * pitch + col * 2;
-                if constexpr (INTER) {
-                    uint32_t u[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+                if (turns && INTER) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < W / 2; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
-                        const float2 e = rot_unpack<BF16>(u[2 * i]), f = rot_unpack<BF16>(u[2 * i + 1]);
-                        if (full || col * 4 + 2 * i < p.half) u[2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
-                        if (full || col * 4 + 2 * i + 1 < p.half) u[2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
+                        const float2 e = rot_unpack<BF16>(a[k][2 * i]), f = rot_unpack<BF16>(a[k][2 * i + 1]);
+                        if (full || col * W + 2 * i < p.half) a[k][2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
+                        if (full || col * W + 2 * i + 1 < p.half) a[k][2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
                     }
-                    *reinterpret_cast<uint4*>(to[k]) = make_uint4(u[0], u[1], u[2], u[3]);
-                } else {
-                    float x1[8], x2[8];
-                    rot_unpack8<BF16>(a[k], x1);
-                    rot_unpack8<BF16>(b[k], x2);
-                    uint32_t w1[4], w2[4];
+                } else if (turns) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < W; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
-                        w1[i] = pack2<BF16>(x1[2 * i] * q.x - x2[2 * i] * q.y, x1[2 * i + 1] * q.z - x2[2 * i + 1] * q.w);
-                        w2[i] = pack2<BF16>(x2[2 * i] * q.x + x1[2 * i] * q.y, x2[2 * i + 1] * q.z + x1[2 * i + 1] * q.w);
+                        const float2 x1 = rot_unpack<BF16>(a[k][i]), x2 = rot_unpack<BF16>(b[k][i]);
+                        a[k][i] = pack2<BF16>(x1.x * q.x - x2.x * q.y, x1.y * q.z - x2.y * q.w);
+                        b[k][i] = pack2<BF16>(x2.x * q.x + x1.x * q.y, x2.y * q.z + x1.y * q.w);
                     }
-                    *reinterpret_cast<uint4*>(to[k]) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                    *reinterpret_cast<uint4*>(to[k] + p.half) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+                    store_words<W>(to[k] + p.half, b[k]);
                 }
+                store_words<W>(to[k], a[k]);
             }
         }
     }
@@ -235,13 +234,16 @@ cudaError_t launch_rotary(const RotaryParams& p0, bool bf16, bool interleaved, i
     int gy = gx < nsm ? (int)((2 * nsm + gx - 1) / gx) : 1;
     gy = gy > heads ? heads : gy;
     const dim3 grid((unsigned)gx, (unsigned)gy), block(kRotThreads);
-    if (!interleaved && p.half % 8 != 0)
+    if (!interleaved && p.half % 4 != 0)
         return bf16 ? launch_early(rotary_pairs_kernel<true>, grid, block, 0, st, p) : launch_early(rotary_pairs_kernel<false>, grid, block, 0, st, p);
     if (interleaved)
-        return bf16 ? launch_early(rotary_columns_kernel<true, true>, grid, block, 0, st, p)
-                    : launch_early(rotary_columns_kernel<false, true>, grid, block, 0, st, p);
-    return bf16 ? launch_early(rotary_columns_kernel<true, false>, grid, block, 0, st, p)
-                : launch_early(rotary_columns_kernel<false, false>, grid, block, 0, st, p);
+        return bf16 ? launch_early(rotary_columns_kernel<true, true, 4>, grid, block, 0, st, p)
+                    : launch_early(rotary_columns_kernel<false, true, 4>, grid, block, 0, st, p);
+    if (p.half % 8 != 0)
+        return bf16 ? launch_early(rotary_columns_kernel<true, false, 2>, grid, block, 0, st, p)
+                    : launch_early(rotary_columns_kernel<false, false, 2>, grid, block, 0, st, p);
+    return bf16 ? launch_early(rotary_columns_kernel<true, false, 4>, grid, block, 0, st, p)
+                : launch_early(rotary_columns_kernel<false, false, 4>, grid, block, 0, st, p);
 }
 
 }  // namespace fa

@@ -60,7 +60,8 @@ ROTARY = [  # B, HQ, HK, S, D, rot, interleaved, dtype, first position
     (1, 2, 1, 129, 192, 192, True, "bf16", 100000), (3, 1, 1, 70, 256, 32, False, "f16", -64),
     (1, 1, 1, 3, 1024, 1024, False, "bf16", 12345), (1, 1, 1, 2, 1024, 1022, True, "f16", 5),
     (1, 16, 16, 1000, 64, 64, False, "bf16", 0), (7, 3, 2, 5, 16, 16, False, "bf16", 9),
-    (1, 2, 1, 40, 40, 16, False, "bf16", 9), (2, 2, 0, 21, 64, 48, True, "bf16", 9),
+    (1, 2, 1, 40, 40, 16, False, "bf16", 9), (2, 3, 1, 50, 192, 24, False, "f16", 9), (1, 2, 2, 9, 1024, 8, False, "bf16", 1),
+    (1, 3, 2, 77, 64, 26, False, "bf16", 50), (1, 1, 1, 20, 128, 120, False, "f16", 3), (2, 2, 0, 21, 64, 48, True, "bf16", 9),
 ]
 
 
