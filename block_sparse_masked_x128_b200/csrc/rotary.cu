@@ -18,6 +18,8 @@
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 namespace fa {
@@ -189,23 +191,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_pairs_kernel(const __grid_
     rot_table(p, cs, tile.b, tile.t0, tile.nt, p.half, [](int j) { return j; });
     __syncthreads();
     const int items = p.half + (p.in_place ? 0 : p.D - 2 * p.half);     // of a row: pairs, then copied elements
-    const int nh = tile.h1 - tile.h0;
-    for (int64_t it = threadIdx.x; it < (int64_t)tile.nt * nh * items; it += kRotThreads) {
-        const int j = (int)(it % items), rw = (int)(it / items);
-        const int t = rw / nh, head = tile.h0 + rw - t * nh;
-        const int w = head >= p.H[0], h = w ? head - p.H[0] : head, s = tile.t0 + t;
-        const uint16_t* x = p.x[w] + tile.b * p.xs[w][0] + h * p.xs[w][1] + s * p.xs[w][2];
-        uint16_t* y = p.y[w] + tile.b * p.ys[w][0] + h * p.ys[w][1] + s * p.ys[w][2];
-        if (j < p.half) {
-            const float2 v = cs[t * p.half + j];
-            const float x1 = rot_unpack<BF16>(x[j]).x, x2 = rot_unpack<BF16>(x[j + p.half]).x;
-            const uint32_t u = pack2<BF16>(x1 * v.x - x2 * v.y, x2 * v.x + x1 * v.y);
-            y[j] = (uint16_t)(u & 0xFFFFu);
-            y[j + p.half] = (uint16_t)(u >> 16);
-        } else {
-            y[j + p.half] = x[j + p.half];
+    const int wide = min(items, kRotThreads), first = threadIdx.x / wide, step = kRotThreads / wide;
+    const int nh = tile.h1 - tile.h0, rows = first < step ? tile.nt * nh : 0;
+    for (int j = threadIdx.x - first * wide; j < items; j += kRotThreads)
+        for (int rw = first; rw < rows; rw += step) {
+            const int t = rw / nh, head = tile.h0 + rw - t * nh;
+            const int w = head >= p.H[0], h = w ? head - p.H[0] : head, s = tile.t0 + t;
+            const uint16_t* x = p.x[w] + tile.b * p.xs[w][0] + h * p.xs[w][1] + s * p.xs[w][2];
+            uint16_t* y = p.y[w] + tile.b * p.ys[w][0] + h * p.ys[w][1] + s * p.ys[w][2];
+            if (j < p.half) {
+                const float2 v = cs[t * p.half + j];
+                const float x1 = rot_unpack<BF16>(x[j]).x, x2 = rot_unpack<BF16>(x[j + p.half]).x;
+                const uint32_t u = pack2<BF16>(x1 * v.x - x2 * v.y, x2 * v.x + x1 * v.y);
+                y[j] = (uint16_t)(u & 0xFFFFu);
+                y[j + p.half] = (uint16_t)(u >> 16);
+            } else {
+                y[j + p.half] = x[j + p.half];
+            }
         }
-    }
 }
 
 }  // namespace
@@ -223,14 +226,16 @@ cudaError_t launch_rotary(const RotaryParams& p0, bool bf16, bool interleaved, i
         }
         p.pos_token_stride = p.pos ? p.pos_stride : 0;
     }
-    // Tokens a CTA: as the table holds them, up to 16, fewer while that leaves SMs without CTAs.
+    // Tokens a CTA: as the table holds them, up to 16 or, with few heads, some 512 rows (a CTA's
+    // latencies need work beside them: 65536 tokens of two heads, 18 us against 33 with 16 tokens),
+    // fewer while that leaves SMs without CTAs.
+    const int heads = p.H[0] + p.H[1];
     int tt = kRotTable / ((p.half + 7) / 8 * 8);
-    tt = tt > 16 ? 16 : tt;
+    tt = std::min(tt, std::max(16, 512 / heads));
     while (tt > 1 && (int64_t)p.B * ((p.S + tt - 1) / tt) < 4 * nsm) tt /= 2;
     p.tokens_per_cta = tt;
     p.ctas_per_seq = (p.S + tt - 1) / tt;
     const int64_t gx = (int64_t)p.B * p.ctas_per_seq;       // at most the tokens: fewer than 2^31
-    const int heads = p.H[0] + p.H[1];
     int gy = gx < nsm ? (int)((2 * nsm + gx - 1) / gx) : 1;
     gy = gy > heads ? heads : gy;
     const dim3 grid((unsigned)gx, (unsigned)gy), block(kRotThreads);
