@@ -8,7 +8,7 @@
 // taken of a 32-bit fraction in [-1/2, 1/2) turns.
 //
 // Bound by HBM (2 bytes read and 2 written an element): 40 heads x 32768 tokens of D = 128, half of
-// it turned, 119 us, 5.65 TB/s or 0.86 of the copy rate; 32 heads x 8192 tokens of D = 64, 14.3 us
+// it turned, 114 us, 5.86 TB/s or 0.89 of the copy rate; 32 heads x 8192 tokens of D = 64, 13.1 us
 // with the launch.  A CTA takes a few tokens of every head: their cos and sin are computed once into
 // shared memory and serve all heads of q and k.  Work goes in columns of 16 bytes (half layout: the
 // two columns of eight pairs; of 8 bytes where rot_dim is a multiple of 8 but not of 16): a thread
@@ -226,15 +226,17 @@ cudaError_t launch_rotary(const RotaryParams& p0, bool bf16, bool interleaved, i
         }
         p.pos_token_stride = p.pos ? p.pos_stride : 0;
     }
-    // Tokens a CTA: as the table holds them, up to 16 or, with few heads, some 512 rows (a CTA's
-    // latencies need work beside them: 65536 tokens of two heads, 18 us against 33 with 16 tokens),
-    // fewer while that leaves SMs without CTAs.
+    // Tokens a CTA.  A CTA's latencies need work beside them, so few CTAs an SM (2048 tokens of 32
+    // heads, D = 64: 5.0 us with two an SM, 6.4 with four, 8.4 with eight), four where two would take
+    // more tokens than 16 or, with few heads, some 512 rows (8192 tokens: 13.1 us, with two 14.2; 65536
+    // tokens of two heads: 18 us, with 16 tokens 33), and no more than that or the table holds.
     const int heads = p.H[0] + p.H[1];
-    int tt = kRotTable / ((p.half + 7) / 8 * 8);
-    tt = std::min(tt, std::max(16, 512 / heads));
-    while (tt > 1 && (int64_t)p.B * ((p.S + tt - 1) / tt) < 4 * nsm) tt /= 2;
-    p.tokens_per_cta = tt;
-    p.ctas_per_seq = (p.S + tt - 1) / tt;
+    const int64_t tokens = (int64_t)p.B * p.S;
+    const int most = std::min(kRotTable / ((p.half + 7) / 8 * 8), std::max(16, 512 / heads));
+    int64_t tt = (tokens + 2 * nsm - 1) / (2 * nsm);
+    if (tt > most) tt = std::min<int64_t>(most, (tokens + 4 * nsm - 1) / (4 * nsm));
+    p.tokens_per_cta = (int)tt;
+    p.ctas_per_seq = (int)((p.S + tt - 1) / tt);
     const int64_t gx = (int64_t)p.B * p.ctas_per_seq;       // at most the tokens: fewer than 2^31
     int gy = gx < nsm ? (int)((2 * nsm + gx - 1) / gx) : 1;
     gy = gy > heads ? heads : gy;
