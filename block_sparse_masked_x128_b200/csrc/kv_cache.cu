@@ -12,7 +12,7 @@
 //
 // Reading moves its bytes once and is bound by HBM (16 sequences of 1k-8k tokens, 16 heads, s8 to
 // bf16: 201 us for 1.31 GB, 0.99 of the copy rate).  Appending is bound by its instructions as much
-// (15k tokens of 8 heads to e4m3: 19 us for 95 MB; 16-bit magnitudes compared two at a time, 32-bit
+// (15k tokens of 8 heads to e4m3: 18 us for 95 MB; 16-bit magnitudes compared two at a time, 32-bit
 // positions and eight lanes a row took two thirds of them away).  A row belongs to eight or D / 8
 // lanes, so its maximum is a few shuffles and nothing is staged; rows of k and v at the same place go
 // together.  The read has two rows of each in flight (four: 52.7 us against 49.6 for a prompt's write
