@@ -167,7 +167,7 @@ struct SeqRange {
 };
 __device__ __forceinline__ SeqRange seq_range(const CacheDecodeParams& p, int b, int sub) {
     SeqRange r;
-    const int n = __ldg(p.kv_lens + b);
+    const int n = p.kv_lens[b];
     if ((unsigned)n > (unsigned)p.c.capacity) g_cache_decode_status = 2;
     r.len = max(0, min(n, p.c.capacity));
     r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
@@ -396,7 +396,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
         for (int u = 0; u < C::sub; ++u) {
             const int key0 = (ld.tile + u) * kTileKeys;
-            page[u] = key0 < ld.sr.len ? __ldg(ld.table + (key0 >> p.c.page_shift)) : 0;
+            page[u] = key0 < ld.sr.len ? ld.table[key0 >> p.c.page_shift] : 0;
         }
     };
     auto enter_head = [&]() {
@@ -529,7 +529,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 slope[nt][j] = 0.f;
                 if ((p.score_kind & FA_SCORE_ALIBI) && nt * 8 + 2 * c + j < cols) {
                     const int hq = hq0 + nt * 8 + 2 * c + j;
-                    slope[nt][j] = kCdLog2e * (p.alibi_slopes ? __ldg(p.alibi_slopes + hq) : exp2f(-8.f * (float)(hq + 1) / (float)p.HQ));
+                    slope[nt][j] = kCdLog2e * (p.alibi_slopes ? p.alibi_slopes[hq] : exp2f(-8.f * (float)(hq + 1) / (float)p.HQ));
                 }
             }
         }

@@ -146,10 +146,10 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     const int sub = threadIdx.x % LPR;
     const int s = blockIdx.x * RPC + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
-    const int count = p.limit ? min(__ldg(p.limit + b), p.S) : p.S;
+    const int count = p.limit ? min(p.limit[b], p.S) : p.S;
     if ((int)(blockIdx.x * RPC) >= count) return;
     // A position start + s, as 32 bits without sign: past the capacity where it is negative.
-    const uint32_t pos = (uint32_t)__ldg(p.start + b) + s;
+    const uint32_t pos = (uint32_t)p.start[b] + s;
     uint4 raw[2][P];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
     const int sub = threadIdx.x % LPR;
     const int s0 = blockIdx.x * RPC * kReadAhead + threadIdx.x / LPR;
     const int h = blockIdx.y, b = blockIdx.z;
-    const uint32_t start = p.start ? __ldg(p.start + b) : 0;
-    const int len = __ldg(p.limit + b);
+    const uint32_t start = p.start ? p.start[b] : 0;
+    const int len = p.limit[b];
     const int32_t* table = p.c.table + (int64_t)b * p.c.table_stride;
     uint4 raw[kReadAhead][2];
     float scale[kReadAhead][2];

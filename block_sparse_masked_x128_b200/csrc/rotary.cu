@@ -54,10 +54,24 @@ __device__ __forceinline__ uint16_t rot_round(float v) {
 // b, pair j of token t at cs[t * pitch + place(j)].
 template <class Place>
 __device__ __forceinline__ void rot_table(const RotaryParams& p, float2* cs, int b, int t0, int nt, int pitch, Place&& place) {
-    for (int i = threadIdx.x; i < nt * p.half; i += kRotThreads) {
-        const int t = i / p.half, j = i - t * p.half, s = t0 + t;
-        const int64_t pos = p.pos ? (int64_t)__ldg(p.pos + b * p.pos_stride + s * p.pos_token_stride) : p.pos0 + s * p.pos_token_stride;
-        cs[t * pitch + place(j)] = rotary_cos_sin(__ldg(p.freq + j), pos, p.factor, p.inverse != 0);
+    constexpr int kEntries = 4;                     // of a thread whose loads are in flight at once
+    const int n = nt * p.half;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kEntries * kRotThreads) {
+        double freq[kEntries];
+        int64_t pos[kEntries];
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k) {
+            const int i = i0 + k * kRotThreads, t = i / p.half, s = t0 + t;
+            if (i >= n) break;
+            freq[k] = p.freq[i - t * p.half];
+            pos[k] = p.pos ? (int64_t)p.pos[b * p.pos_stride + s * p.pos_token_stride] : p.pos0 + s * p.pos_token_stride;
+        }
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k) {
+            const int i = i0 + k * kRotThreads, t = i / p.half;
+            if (i >= n) break;
+            cs[t * pitch + place(i - t * p.half)] = rotary_cos_sin(freq[k], pos[k], p.factor, p.inverse != 0);
+        }
     }
 }
 

@@ -88,7 +88,9 @@ cudaError_t cache_decode_status(cudaStream_t st, int32_t* out);
 // The kernels of these operators are short and follow one another: each is launched so that it may
 // start before its predecessor on the stream ends, and its first act is to wait for that end
 // (with all the predecessor's writes) before it reads or writes anything.  What overlaps is the
-// launch.  A kernel that comes to grid_dependency_release in all its blocks lets its successor
+// launch.  The predecessor may write what they read (positions, lengths, tables, rows) while they
+// are already on the SMs, so they load it as memory that changes, not by __ldg, whose data must stay
+// the same for a kernel's whole life.  A kernel that comes to grid_dependency_release in all its blocks lets its successor
 // start there rather than at its own end.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -112,7 +114,7 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_
 // the row does not reach it or names a page outside the pool.
 __device__ __forceinline__ int cache_page(const CacheView& c, const int32_t* table, uint32_t pos) {
     if (pos >= (uint32_t)c.capacity) return -1;
-    const int page = __ldg(table + (pos >> c.page_shift));
+    const int page = table[pos >> c.page_shift];
     return (unsigned)page < (unsigned)c.n_pages ? page : -1;
 }
 #endif
