@@ -231,6 +231,16 @@ __device__ __forceinline__ Run find_run(const CacheDecodeParams& p, int sub, int
     return r;
 }
 
+// cap tanh(y) of x = cap y, both in log2 units; k = 2 / cap takes x to 2 y log2 e.  From |y| = 1/4 on it
+// is cap (1 - 2 / (e^2y + 1)), which is off by some 2^-23 of cap; below, x times the series of
+// tanh(y) / y (its next term: 2^-26), so that scores far below a large cap keep their bits.
+__device__ __forceinline__ float soft_cap(float x, float k, float cap_log2) {
+    const float z = x * k, u = z * z * 0.12011325347955035f;       // u = y^2
+    const float series = fmaf(fmaf(fmaf(0.021869488f, u, -0.053968254f), u, 0.13333333f), u, -0.33333333f);
+    const float far = cap_log2 * (1.f - __fdividef(2.f, ex2_approx(z > 120.f ? 120.f : z) + 1.f));
+    return fabsf(z) < 0.72f ? fmaf(x * u, series, x) : far;
+}
+
 // The head groups of a kv head: columns of the products, `rows` of them at a time.
 __host__ __device__ constexpr int col_blocks(int group, int cols) { return (group + cols - 1) / cols; }
 
@@ -603,11 +613,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            // cap tanh(y) = cap (1 - 2 / (e^2y + 1)); softcap_k takes x to 2 y log2 e.
-                            if (p.score_kind & FA_SCORE_SOFTCAP) {
-                                const float y = x[u][nt][i] * p.softcap_k;
-                                x[u][nt][i] = p.softcap_log2 * (1.f - __fdividef(2.f, ex2_approx(y > 120.f ? 120.f : y) + 1.f));
-                            }
+                            if (p.score_kind & FA_SCORE_SOFTCAP) x[u][nt][i] = soft_cap(x[u][nt][i], p.softcap_k, p.softcap_log2);
                             if (p.score_kind & FA_SCORE_ALIBI)
                                 x[u][nt][i] = fmaf(slope[nt][i & 1], (float)(key + 8 * (i >> 1) - (sr.len - 1)), x[u][nt][i]);
                         }

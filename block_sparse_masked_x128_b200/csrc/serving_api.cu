@@ -370,7 +370,7 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
     p.window = window;
     p.scale_log2 = (float)(sc * log2e);
     p.softcap_log2 = (float)(cap * log2e);
-    p.softcap_k = (float)(2.0 / cap);
+    p.softcap_k = (float)std::fmin(2.0 / cap, 3.4028234663852886e38);     // of a subnormal cap
     p.alibi_slopes = params ? params->alibi_slopes : nullptr;
     p.score_kind = (int32_t)score_mod_kind;
     p.workspace = workspace;

@@ -420,6 +420,18 @@ def test_decode_score_mods(kind, mod, window):
         check_decode(q, out, lse, K, V, lens, window, 20.0 if mod & 1 else None, s64, 0.2, kind)
 
 
+@pytest.mark.parametrize("cap", [1e-41, 1e-3, 4.0, 3e3, 1e6, math.inf])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_decode_soft_caps_of_any_size(kind, cap):
+    # A cap far above the scores changes nothing (an infinite one: at all); one far below leaves signs.
+    fa = fa_module()
+    lens = [1, 40, 700]
+    cache, table, K, V = random_cache(kind, lens, 32, 2, 64, seed=5, scale=2.0)
+    q = rand((3, 6, 1, 64), torch.bfloat16, 3, 3.0)
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens), score_mod=fa.FA_SCORE_SOFTCAP, softcap=cap, scale=0.2)
+    check_decode(q, out, lse, K, V, lens, softcap=None if math.isinf(cap) else cap, scale=0.2, kind=kind)
+
+
 @pytest.mark.parametrize("B, HQ, H, n, long", [(40, 64, 4, 60, 9000), (300, 12, 1, 40, 0), (3, 96, 2, 700, 0), (30, 2, 2, 30, 20000),
                                                   (2, 1024, 1, 500, 0)])
 def test_decode_many_heads_and_one_long_sequence(B, HQ, H, n, long):
