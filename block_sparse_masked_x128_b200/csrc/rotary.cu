@@ -8,10 +8,11 @@
 // taken of a 32-bit fraction in [-1/2, 1/2) turns.
 //
 // Bound by HBM (2 bytes read and 2 written an element): 40 heads x 32768 tokens of D = 128, half of
-// it turned, 114 us, 5.86 TB/s or 0.89 of the copy rate; 32 heads x 8192 tokens of D = 64, 13.1 us
+// it turned, 115 us, 5.84 TB/s or 0.89 of the copy rate; 32 heads x 8192 tokens of D = 64, 13.1 us
 // with the launch.  A CTA takes a few tokens of every head: their cos and sin are computed once into
 // shared memory and serve all heads of q and k.  Work goes in columns of 16 bytes (half layout: the
-// two columns of eight pairs; of 8 bytes where rot_dim is a multiple of 8 but not of 16): a thread
+// two columns of eight pairs; of 8 bytes where rot_dim is a multiple of 8 but not of 16, the copied
+// rest in 16 all the same: 10 x 1833 tokens of 32 heads, 24 of 192 elements, 80 us, 107 before): a thread
 // keeps its column and walks the rows (token, head) by fixed offsets, with the loads of kAhead rows
 // in flight (twice as many: 20.5 us at 8192 tokens).  Pairs that do not fill such columns (half
 // layout with rot_dim no multiple of 8) go one by one.
@@ -92,7 +93,7 @@ __device__ __forceinline__ RotTile rot_tile(const RotaryParams& p) {
 
 // W words as one access.
 template <int W>
-__device__ __forceinline__ void load_words(const uint16_t* x, uint32_t (&w)[W]) {
+__device__ __forceinline__ void load_words(const uint16_t* x, uint32_t* w) {
     if constexpr (W == 4) {
         const uint4 v = *reinterpret_cast<const uint4*>(x);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -102,7 +103,7 @@ __device__ __forceinline__ void load_words(const uint16_t* x, uint32_t (&w)[W]) 
     }
 }
 template <int W>
-__device__ __forceinline__ void store_words(uint16_t* y, const uint32_t (&w)[W]) {
+__device__ __forceinline__ void store_words(uint16_t* y, const uint32_t* w) {
     if constexpr (W == 4) *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
     else *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
 }
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
     // The columns of a row: rotated ones (half layout: pairs of columns), then copied ones.
     const int rot_cols = (p.half + J - 1) / J;
     const int copied0 = INTER ? rot_cols * E : 2 * p.half;
-    const int cols = rot_cols + (p.in_place ? 0 : (p.D - copied0) / E);
+    const int cols = rot_cols + (p.in_place ? 0 : (p.D - copied0) / 8);        // copied ones are of 16 bytes
     const int col = threadIdx.x % cols, first = threadIdx.x / cols, stride = kRotThreads / cols;   // D <= 1024: cols <= 256
     // Two pairs of all columns stand together: neighbouring columns read neighbouring 16 bytes.
     const int pitch = rot_cols * J;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
     __syncthreads();
     if (first >= stride) return;
     const bool turns = col < rot_cols, full = !INTER || col * W + W <= p.half;
-    const int at = turns ? col * E : copied0 + (col - rot_cols) * E;
+    const int at = turns ? col * E : copied0 + (col - rot_cols) * 8;
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {                  // q, k
         const int hb = w ? p.H[0] : 0;
@@ -146,14 +147,15 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
         const int64_t x_step = in_step * xi + out_step * xo, x_wrap = xo - inner * xi;
         const int64_t y_step = in_step * yi + out_step * yo, y_wrap = yo - inner * yi;
         for (int rw = first; rw < rows; rw += stride * kAhead) {
-            uint32_t a[kAhead][W], b[kAhead][W];
+            uint32_t v[kAhead][2 * W];      // a column and, in half layout, its pairs' other halves
             int token[kAhead];
             uint16_t* to[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (rw + k * stride < rows) {
-                    load_words<W>(x, a[k]);
-                    if (!INTER && turns) load_words<W>(x + p.half, b[k]);
+                    if (turns || W == 4) load_words<W>(x, v[k]);
+                    else load_words<4>(x, v[k]);
+                    if (!INTER && turns) load_words<W>(x + p.half, v[k] + W);
                 }
                 token[k] = tok_in ? in : out;
                 to[k] = y;
@@ -171,26 +173,27 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (rw + k * stride >= rows) break;
-                const float2* v = cs + token[k] * pitch + col * 2;
+                const float2* turn = cs + token[k] * pitch + col * 2;
                 if (turns && INTER) {
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) {
-                        const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
-                        const float2 e = rot_unpack<BF16>(a[k][2 * i]), f = rot_unpack<BF16>(a[k][2 * i + 1]);
-                        if (full || col * W + 2 * i < p.half) a[k][2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
-                        if (full || col * W + 2 * i + 1 < p.half) a[k][2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
+                        const float4 q = *reinterpret_cast<const float4*>(turn + i * rot_cols * 2);
+                        const float2 e = rot_unpack<BF16>(v[k][2 * i]), f = rot_unpack<BF16>(v[k][2 * i + 1]);
+                        if (full || col * W + 2 * i < p.half) v[k][2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
+                        if (full || col * W + 2 * i + 1 < p.half) v[k][2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
                     }
                 } else if (turns) {
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
-                        const float4 q = *reinterpret_cast<const float4*>(v + i * rot_cols * 2);
-                        const float2 x1 = rot_unpack<BF16>(a[k][i]), x2 = rot_unpack<BF16>(b[k][i]);
-                        a[k][i] = pack2<BF16>(x1.x * q.x - x2.x * q.y, x1.y * q.z - x2.y * q.w);
-                        b[k][i] = pack2<BF16>(x2.x * q.x + x1.x * q.y, x2.y * q.z + x1.y * q.w);
+                        const float4 q = *reinterpret_cast<const float4*>(turn + i * rot_cols * 2);
+                        const float2 x1 = rot_unpack<BF16>(v[k][i]), x2 = rot_unpack<BF16>(v[k][W + i]);
+                        v[k][i] = pack2<BF16>(x1.x * q.x - x2.x * q.y, x1.y * q.z - x2.y * q.w);
+                        v[k][W + i] = pack2<BF16>(x2.x * q.x + x1.x * q.y, x2.y * q.z + x1.y * q.w);
                     }
-                    store_words<W>(to[k] + p.half, b[k]);
+                    store_words<W>(to[k] + p.half, v[k] + W);
                 }
-                store_words<W>(to[k], a[k]);
+                if (turns || W == 4) store_words<W>(to[k], v[k]);
+                else store_words<4>(to[k], v[k]);
             }
         }
     }
