@@ -272,7 +272,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor ws;
         if (a[12] != Py_None) {
             ws = tensor(a[12], "workspace");
-            require(cuda_index(ws) == device, "workspace must be on the cache's device");
+            // Its bytes have to be its own: a strided or broadcast tensor counts more than its memory holds.
+            require(cuda_index(ws) == device && ws.is_contiguous(), "workspace must be a contiguous tensor on the cache's device");
         } else {
             ws = at::empty({(int64_t)g_entry.decode_bytes(dq.B, dq.H, c->H, dq.D)}, q.options().dtype(at::kByte));
         }
