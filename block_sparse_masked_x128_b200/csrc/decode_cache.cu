@@ -146,6 +146,15 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return make_float2(__half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))), __half2float(__ushort_as_half((unsigned short)(w >> 16))));
 }
 
+// Two 16-bit values with infinities as the largest finite ones.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    uint32_t d;
+    if constexpr (BF16) asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x7F7F7F7Fu));
+    else asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x7BFF7BFFu));
+    return d;
+}
+
 // Bytes 2 HI and 2 HI + 1 of four codes as two fp16 values, exactly.  s8: the code plus 128 in the
 // low byte of 1024 = 0x6400, whose unit is 1, less 1152.
 template <int DT, int HI>
@@ -677,7 +686,9 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             for (int u = 0; u < C::sub; ++u) {
                 // The weights' transpose is the second operand.  For 16-bit caches, whose products have
                 // time to spare, a weight goes as two numbers, itself rounded and the rest: 8 bits of
-                // it in bf16 alone put the result's error at 1.3 times that of its own rounding.
+                // it in bf16 alone put the result's error at 1.3 times that of its own rounding.  A positive
+                // weight's first number is positive (fp16's least, 2^-24, at least; the rest, which may be
+                // negative, makes up for it) and alone meets infinite values, so that they stay infinite.
                 constexpr int PARTS = C::k8 ? 1 : 2;
                 uint32_t pb[PARTS][NT][2];
 #pragma unroll
@@ -686,7 +697,8 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     for (int i = 0; i < 2; ++i) {
                         l[nt][0] += e2[u][nt][2 * i];
                         l[nt][1] += e2[u][nt][2 * i + 1];
-                        const uint32_t two = pack2<BF16>(w[u][nt][2 * i], w[u][nt][2 * i + 1]);
+                        auto first = [](float w) { return DT == FA_DTYPE_F16 && w > 0.f ? fmaxf(w, 0x1p-24f) : w; };
+                        const uint32_t two = pack2<BF16>(first(w[u][nt][2 * i]), first(w[u][nt][2 * i + 1]));
                         pb[0][nt][i] = transpose8x8(two);
                         if constexpr (!C::k8) {
                             const float2 r2 = unpack2<BF16>(two);
@@ -732,9 +744,10 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             const uint32_t a0 = __byte_perm(v[0][q], v[1][q], 0x5410), a1 = __byte_perm(v[0][q], v[1][q], 0x7632);
                             const uint32_t a2 = __byte_perm(v[2][q], v[3][q], 0x5410), a3 = __byte_perm(v[2][q], v[3][q], 0x7632);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+                            const uint32_t f0 = finite2<BF16>(a0), f1 = finite2<BF16>(a1), f2 = finite2<BF16>(a2), f3 = finite2<BF16>(a3);
 #pragma unroll
-                                for (int k = 0; k < PARTS; ++k) mma16816<BF16>(o[nt][4 * e + q], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[nt][4 * e + q], f0, f1, f2, f3, pb[1][nt][0], pb[1][nt][1]);
                         }
                     }
                 }

@@ -45,3 +45,61 @@ def test_decode_refuses_a_workspace_that_is_not_contiguous():
     torch.cuda.synchronize()
 
 
+# ---------------------------------------------------------------- infinities in 16-bit caches
+
+@pytest.mark.parametrize("lens", [NARROW, WIDE], ids=["narrow", "wide"])
+@pytest.mark.parametrize("kind, D, group", [("bf16", 128, 1), ("f16", 64, 3), ("f16", 128, 12), ("bf16", 64, 9)])
+def test_decode_infinite_values_stay_infinite(kind, D, group, lens):
+    # sum p v of a value +inf is +inf however small its weight (here at least e^-30), -inf likewise,
+    # NaN where both meet; other elements, heads and sequences are as without them.
+    fa = fa_module()
+    cache, table, K, V = random_cache(kind, lens, 16, 2, D, seed=group)
+    for b, n in enumerate(lens):
+        for key in {0, n // 2, n - 1}:
+            put(cache, table, b, key, 1, 3, math.inf)
+            put(cache, table, b, key, 1, D - 1, -math.inf)
+        put(cache, table, b, 0, 1, 8, math.inf)
+        put(cache, table, b, n - 1, 1, 8, -math.inf)
+        V[b][1][:, [3, 8, D - 1]] = 0
+    q = rand((len(lens), 2 * group, 1, D), TYPES[kind], 9, 1.5)
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    hit = out[:, group:, 0]
+    assert (hit[..., 3] == math.inf).all() and (hit[..., D - 1] == -math.inf).all()
+    assert torch.isnan(hit[1:, :, 8]).all() and (hit[0, :, 8] == -math.inf).all()
+    hit[..., [3, 8, D - 1]] = 0
+    check_decode(q, out, lse, K, V, lens, kind=kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_decode_infinite_values_with_light_weights(kind):
+    # Weights from 1 down to 2^-60: far below what fp16 holds.
+    fa = fa_module()
+    for n in (40, 2000):
+        cache, table, _, _ = random_cache(kind, [n], 16, 1, 64, seed=n)
+        cache.k.zero_()
+        cache.v.copy_(torch.zeros_like(cache.v))
+        for i in range(n):                       # score of key i: -(i % 61) ln 2
+            cache.k[table[0, i // 16].item(), 0, i % 16, 0] = -(i % 61) / 4.0
+        q = torch.zeros(1, 1, 1, 64, dtype=TYPES[kind], device="cuda")
+        q[..., 0] = 1.0
+        for i in range(40):
+            put(cache, table, 0, i, 0, i, math.inf if i % 2 else -math.inf)
+        out, lse = fa.decode_attention(q, cache, table, i32(n), scale=4 * math.log(2.0))
+        want = torch.tensor([math.inf if i % 2 else -math.inf for i in range(40)] + [0.0] * 24, device="cuda")
+        assert torch.equal(out[0, 0, 0].float(), want), out
+        total = sum(2.0 ** -(i % 61) for i in range(n))
+        assert abs(float(lse) - math.log(total)) <= 1e-4
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [60, 2000])
+def test_decode_masked_infinite_values_and_scores_count_for_nothing(kind, n):
+    fa = fa_module()
+    cache, table, K, V = random_cache(kind, [n], 16, 1, 64, seed=2, garbage=False)
+    q = rand((1, 4, 1, 64), TYPES[kind], 3)
+    at = n - 30
+    for key in (0, at - 11, at - 1):
+        put(cache, table, 0, key, 0, 5, math.inf)
+        cache.k[table[0, key // 16].item(), 0, key % 16, 7] = math.inf
+    out, lse = fa.decode_attention(q, cache, table, i32(n), window=30)
+    check_decode(q, out, lse, K, V, [n], 30, kind=kind)
