@@ -31,9 +31,10 @@
 //   Softmax    a head's weights are w_j = 2^(x_j - m) vscale_j; for the product they become one fp16
 //              number over 8-bit caches, two 16-bit numbers over 16-bit ones (the sum of the
 //              2^(x_j - m) is fp32).  The reference m is raised, to the largest
-//              x_j + log2 vscale_j so far, only when a weight exceeds 2^8: most tiles need no
-//              reduction over the lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16
-//              at least) or, in fp16, 2^-25 of the largest, however the v scales differ.
+//              x_j + log2 vscale_j so far, only when a weight exceeds 2^8 (bf16 caches: to 8 above
+//              the largest x_j, when one exceeds 1): most tiles need no reduction over the lanes, and
+//              a weight is held to 2^-11 of itself (two numbers: 2^-16 at least) or, in fp16, 2^-25
+//              of the largest, however the v scales differ.
 //
 // Measured (whole calls, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k tokens, bf16,
 // D = 128: 75 us, 6.15 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 234 us, 6.4 TB/s;
@@ -56,7 +57,12 @@ __device__ int32_t g_cache_decode_status;   // 2: a length or page out of range 
 constexpr int kCdWarps = 4, kCdThreads = 32 * kCdWarps;
 constexpr int kTileKeys = 16;               // keys a warp takes at a time
 constexpr float kCdLn2 = 0.6931471805599453f, kCdLog2e = 1.4426950408889634f;
-constexpr float kTopWeight = 256.f;         // weights above this raise the reference
+// A weight above 2^8 raises the reference to the largest score; over a bf16 cache, whose values reach
+// the end of fp32's range, one above 1 raises it to 8 above, so that a weight times a value fits.
+template <int DT>
+constexpr float kTopWeight = DT == FA_DTYPE_BF16 ? 1.f : 256.f;
+template <int DT>
+constexpr float kHeadroom = DT == FA_DTYPE_BF16 ? 8.f : 0.f;
 // Value scales below 2^-90 count as 2^-90 in the reference, which bounds 2^(x - m) by 2^98: the
 // sum over 2^25 keys stays finite.
 constexpr float kMinScaleLog2 = -90.f, kTopSum = 3.169126500570573e29f;
@@ -651,7 +657,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             const float e = ex2_approx(x[u][nt][i] - m[nt][i & 1]);
                             e2[u][nt][i] = e;
                             w[u][nt][i] = C::k8 ? e * vscale[u][i >> 1] : e;
-                            high = high || fabsf(w[u][nt][i]) > kTopWeight || (C::k8 && e > kTopSum);
+                            high = high || fabsf(w[u][nt][i]) > kTopWeight<DT> || (C::k8 && e > kTopSum);
                         }
                 return high;
             };
@@ -667,7 +673,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             for (int i = 0; i < 2; ++i) {
                                 float y = x[u][nt][2 * i + j];
                                 if constexpr (C::k8) y += fmaxf(__log2f(fabsf(vscale[u][i])), kMinScaleLog2);
-                                top = fmaxf(top, y);
+                                top = fmaxf(top, y + kHeadroom<DT>);
                             }
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));

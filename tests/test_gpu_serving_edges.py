@@ -103,3 +103,25 @@ def test_decode_masked_infinite_values_and_scores_count_for_nothing(kind, n):
         cache.k[table[0, key // 16].item(), 0, key % 16, 7] = math.inf
     out, lse = fa.decode_attention(q, cache, table, i32(n), window=30)
     check_decode(q, out, lse, K, V, [n], 30, kind=kind)
+
+
+# ---------------------------------------------------------------- the largest values
+
+@pytest.mark.parametrize("lens", [[500] * 8, MANY], ids=["narrow", "split"])
+def test_decode_largest_bf16_values(lens):
+    # A key some e^4 above the others whose values are bf16's largest: its weight times the value is
+    # within fp32 as long as no weight exceeds 1.
+    fa = fa_module()
+    cache, table, _, _ = random_cache("bf16", lens, 16, 2, 64, seed=3, garbage=False)
+    cache.k.zero_()
+    top = torch.finfo(torch.bfloat16).max
+    for b, n in enumerate(lens):
+        for h in range(2):
+            at = (37 + 61 * b + 29 * h) % n
+            cache.k[table[b, at // 16].item(), h, at % 16, 0] = 4.0
+            for d in range(64):
+                put(cache, table, b, at, h, d, top if d % 2 else -top)
+    q = torch.zeros(len(lens), 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens), scale=1.0)
+    check_decode(q, out, lse, *rows64(cache, table, lens), lens, scale=1.0)
