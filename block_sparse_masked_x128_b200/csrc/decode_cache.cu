@@ -11,7 +11,7 @@
 //              single long sequences load every SM alike.  The lengths are device data: each warp
 //              finds its run by a scan over the sequences.  A run may go through several heads; the
 //              loads run ahead across the border, so a warp's stream of copies never stops.  A head
-//              whose steps are all one warp's is finished by it; otherwise the (m, l, O) of its
+//              whose steps are all one warp's is finished by it; otherwise the (m, l, O / l) of its
 //              part goes to the workspace and the merge kernel joins the parts in key order (no
 //              atomics: the same bits every time).  Warps share nothing and never wait.  Where
 //              the tables map few tokens, a CTA takes a head alone instead and joins its warps' parts
@@ -28,13 +28,15 @@
 //   8 bits     codes become fp16 exactly, in registers.  The key's scale multiplies its score, the
 //              value's scale the weight, both in fp32.  q is brought into fp16's range by a power of
 //              two a head, so it keeps all its bits.
-//   Softmax    a head's weights are w_j = 2^(x_j - m) vscale_j; for the product they become one fp16
-//              number over 8-bit caches, two 16-bit numbers over 16-bit ones (the sum of the
-//              2^(x_j - m) is fp32).  The reference m is raised, to the largest
-//              x_j + log2 vscale_j so far, only when a weight exceeds 2^8 (bf16 caches: to 8 above
-//              the largest x_j, when one exceeds 1): most tiles need no reduction over the lanes, and
-//              a weight is held to 2^-11 of itself (two numbers: 2^-16 at least) or, in fp16, 2^-25
-//              of the largest, however the v scales differ.
+//   Softmax    l sums 2^(x_j - m) in fp32, and O sums w_j v_j with w_j = 2^(x_j - m); over 8-bit
+//              caches w_j code_j with w_j = 2^(x_j - m) (vscale_j u), u a power of two that takes
+//              the largest weight near 1, so neither sum depends on the size of the other's terms.
+//              For the product a weight becomes one fp16 number over 8-bit caches, two 16-bit
+//              numbers over 16-bit ones.  m is raised to the largest x_j so far, and u set by the
+//              largest x_j + log2 vscale_j, only when a weight exceeds 2^8 (bf16 caches: m to 8
+//              above the largest x_j, when one exceeds 1): most tiles need no reduction over the
+//              lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16 at least) or, in
+//              fp16, 2^-25 of the largest, however the v scales differ.
 //
 // Measured (whole calls, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k tokens, bf16,
 // D = 128: 75 us, 6.15 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 234 us, 6.4 TB/s;
@@ -63,9 +65,9 @@ template <int DT>
 constexpr float kTopWeight = DT == FA_DTYPE_BF16 ? 1.f : 256.f;
 template <int DT>
 constexpr float kHeadroom = DT == FA_DTYPE_BF16 ? 8.f : 0.f;
-// Value scales below 2^-90 count as 2^-90 in the reference, which bounds 2^(x - m) by 2^98: the
-// sum over 2^25 keys stays finite.
-constexpr float kMinScaleLog2 = -90.f, kTopSum = 3.169126500570573e29f;
+// Value scales count as 2^-126 to 2^126 in the unit u of O, which is 2^126 to 2^-126 then: every scale
+// that a written row can have, and zeros as fresh pools hold them.
+constexpr float kMaxScaleLog2 = 126.f;
 
 template <int DT, int D, int NT>
 struct CdConfig {
@@ -96,7 +98,7 @@ struct CdConfig {
     static constexpr int smem = kCdWarps * stages * stage;
     static constexpr int seg = k8 && D == 128 ? 16 : 8;   // a lane's dims come in runs of this
     static constexpr int orow = D + D / seg * 4;
-    static_assert(8 * NT * (kCdWarps * (orow + 2) + 2) * 4 <= smem, "join_and_write uses the rings' memory");
+    static_assert(8 * NT * (kCdWarps * (orow + 2) + 1) * 4 <= smem, "join_and_write uses the rings' memory");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {
@@ -143,6 +145,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// 2^k and k of 2^k, for integers -126 <= k <= 126.
+__device__ __forceinline__ float power_of_two(float k) { return __uint_as_float((uint32_t)((int)k + 127) << 23); }
+__device__ __forceinline__ float exponent_of(float u) { return (float)((int)(__float_as_uint(u) >> 23) - 127); }
+
+// a with its magnitude at most that of the largest finite number.
+__device__ __forceinline__ float finite(float a) {
+    float d;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(FLT_MAX));
     return d;
 }
 
@@ -265,19 +278,26 @@ __device__ __forceinline__ int lane_dim(int r, int k) {
     return 2 * k / SEG * 64 + r * SEG + 2 * k % SEG;
 }
 
-// Joins the (m, l, O) of the CTA's warps in shared memory (over the rings, which are done with) and
-// writes the result.
+// What takes a column's O to its average over the keys: 1 / l and 1 / u, apart because either may be
+// as small as fp32 goes (no key: 0).
+struct Average {
+    float inv, unit;
+    __device__ __forceinline__ Average(float l, float u) : inv(l == 0.f ? 0.f : 1.f / l), unit(power_of_two(-exponent_of(u))) {}
+    __device__ __forceinline__ float operator()(float o) const { return o * inv * unit; }
+};
+
+// Joins the parts (m, l, average) of the CTA's warps in shared memory (over the rings, which are done
+// with) and writes the result.
 template <int DT, int D, int NT>
 __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8_t* smem, const float (&o)[NT][D / 16][4], const float (&m)[NT][2],
-                                               const float (&l)[NT][2], int b, int hq0, int cols, bool q_bf16) {
+                                               const float (&unit)[NT][2], const float (&l)[NT][2], int b, int hq0, int cols, bool q_bf16) {
     using C = CdConfig<DT, D, NT>;
     constexpr int COLS = 8 * NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     float* so = reinterpret_cast<float*>(smem);     // [warp][column] rows of D floats, 4 more after each run (bank conflicts)
-    float* sm = so + kCdWarps * COLS * C::orow;     // [warp][column] m, then the factor of O
+    float* sm = so + kCdWarps * COLS * C::orow;     // [warp][column] m, then the average's share
     float* sl = sm + kCdWarps * COLS;               // [warp][column] l
-    float* sM = sl + kCdWarps * COLS;               // [column] M, L
-    float* sL = sM + COLS;
+    float* sL = sl + kCdWarps * COLS;               // [column] L
     cp_async_wait<0>();
     __syncthreads();
 #pragma unroll
@@ -292,11 +312,13 @@ __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8
                 sm[warp * COLS + col] = m[nt][j];
                 sl[warp * COLS + col] = sum;
             }
+            const Average av(sum, unit[nt][j]);
             float* row = so + (warp * COLS + col) * C::orow;
 #pragma unroll
             for (int k = 0; k < D / 16; k += 2) {
                 const int dim = lane_dim<C::seg>(r, k);
-                *reinterpret_cast<float4*>(row + dim + dim / C::seg * 4) = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+                *reinterpret_cast<float4*>(row + dim + dim / C::seg * 4) =
+                    make_float4(av(o[nt][k][j]), av(o[nt][k][2 + j]), av(o[nt][k + 1][j]), av(o[nt][k + 1][2 + j]));
             }
         }
     __syncthreads();
@@ -307,12 +329,15 @@ __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8
         for (int w = 0; w < kCdWarps; ++w) M = fmaxf(M, sm[w * COLS + col]);
 #pragma unroll
         for (int w = 0; w < kCdWarps; ++w) {
-            const float f = ex2_approx(sm[w * COLS + col] - M);
-            L = fmaf(sl[w * COLS + col], f, L);
+            const float f = sl[w * COLS + col] * ex2_approx(sm[w * COLS + col] - M);
+            L += f;
             sm[w * COLS + col] = f;
         }
-        sM[col] = M;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int w = 0; w < kCdWarps; ++w) sm[w * COLS + col] *= inv;
         sL[col] = L;
+        if (col < cols && p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = L == 0.f ? -INFINITY : (M + log2f(L)) * kCdLn2;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < cols * (D / 4); i += kCdThreads) {
@@ -324,12 +349,9 @@ __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8
             const float4 v = *reinterpret_cast<const float4*>(so + (w * COLS + col) * C::orow + dim + dim / C::seg * 4);
             s = make_float4(fmaf(v.x, f, s.x), fmaf(v.y, f, s.y), fmaf(v.z, f, s.z), fmaf(v.w, f, s.w));
         }
-        const float L = sL[col], inv = L == 0.f ? 0.f : 1.f / L;
-        uint2 w = q_bf16 ? make_uint2(pack2<true>(s.x * inv, s.y * inv), pack2<true>(s.z * inv, s.w * inv))
-                         : make_uint2(pack2<false>(s.x * inv, s.y * inv), pack2<false>(s.z * inv, s.w * inv));
-        if (L == 0.f) w = make_uint2(0, 0);
+        uint2 w = q_bf16 ? make_uint2(pack2<true>(s.x, s.y), pack2<true>(s.z, s.w)) : make_uint2(pack2<false>(s.x, s.y), pack2<false>(s.z, s.w));
+        if (sL[col] == 0.f) w = make_uint2(0, 0);
         *reinterpret_cast<uint2*>(p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1] + dim) = w;
-        if (dim == 0 && p.lse) p.lse[(int64_t)b * p.HQ + hq0 + col] = L == 0.f ? -INFINITY : (sM[col] + log2f(L)) * kCdLn2;
     }
 }
 
@@ -558,10 +580,11 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 }
             }
         }
-        float m[NT][2], l[NT][2], o[NT][KS][4];
+        float m[NT][2], ou[NT][2], l[NT][2], o[NT][KS][4];      // ou: the unit of O, 1 over 16-bit caches
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -FLT_MAX;
+            ou[nt][0] = ou[nt][1] = 1.f;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int t = 0; t < KS; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
@@ -644,7 +667,9 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     }
                 }
             }
-            // Weights against the present reference; one that is too large raises it first.
+            // Weights against the present reference and unit; one that is too large changes them first.
+            // (A scale times the unit that leaves fp32 belongs to a key below 2^-120 of the heaviest, or
+            // to one that changes them.)
             float w[C::sub][NT][4], e2[C::sub][NT][4];
             auto weights = [&]() {
                 bool high = false;
@@ -656,8 +681,8 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                         for (int i = 0; i < 4; ++i) {
                             const float e = ex2_approx(x[u][nt][i] - m[nt][i & 1]);
                             e2[u][nt][i] = e;
-                            w[u][nt][i] = C::k8 ? e * vscale[u][i >> 1] : e;
-                            high = high || fabsf(w[u][nt][i]) > kTopWeight<DT> || (C::k8 && e > kTopSum);
+                            w[u][nt][i] = C::k8 ? e * finite(vscale[u][i >> 1] * ou[nt][i & 1]) : e;
+                            high = high || e > kTopWeight<DT> || (C::k8 && fabsf(w[u][nt][i]) > kTopWeight<DT>);
                         }
                 return high;
             };
@@ -666,20 +691,30 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = m[nt][j];
+                        // heavy: log2 of the heaviest weight with its scale, so far 1 / u at m.
+                        float top = m[nt][j], heavy = m[nt][j] - exponent_of(ou[nt][j]);
 #pragma unroll
                         for (int u = 0; u < C::sub; ++u)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                float y = x[u][nt][2 * i + j];
-                                if constexpr (C::k8) y += fmaxf(__log2f(fabsf(vscale[u][i])), kMinScaleLog2);
+                                const float y = x[u][nt][2 * i + j];
                                 top = fmaxf(top, y + kHeadroom<DT>);
+                                if constexpr (C::k8) heavy = fmaxf(heavy, y + fminf(fmaxf(__log2f(fabsf(vscale[u][i])), -kMaxScaleLog2), kMaxScaleLog2));
                             }
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
-                        const float alpha = ex2_approx(m[nt][j] - top);
+                        for (int off = 4; off < 32; off <<= 1) {
+                            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, off));
+                            if constexpr (C::k8) heavy = fmaxf(heavy, __shfl_xor_sync(kFullMask, heavy, off));
+                        }
+                        float shift = m[nt][j] - top;
+                        l[nt][j] *= ex2_approx(shift);
                         m[nt][j] = top;
-                        l[nt][j] *= alpha;
+                        if constexpr (C::k8) {
+                            const float k = fminf(fmaxf(floorf(top - heavy), -kMaxScaleLog2), kMaxScaleLog2);
+                            shift += k - exponent_of(ou[nt][j]);
+                            ou[nt][j] = power_of_two(k);
+                        }
+                        const float alpha = ex2_approx(shift);
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             o[nt][k][j] *= alpha;
@@ -761,10 +796,10 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             slot = slot + 1 == C::stages ? 0 : slot + 1;
         }
         if constexpr (WHOLE) {
-            join_and_write<DT, D, NT>(p, smem, o, m, l, b, hq0, cols, q_bf16);
+            join_and_write<DT, D, NT>(p, smem, o, m, ou, l, b, hq0, cols, q_bf16);
             return;
         }
-        // The part's (m, l, O), or the result.  A worker's first head has slot 2 worker, a later one
+        // The part's (m, l, average), or the result.  A worker's first head has slot 2 worker, a later one
         // that it leaves unfinished slot 2 worker + 1.
         const int part = 2 * worker + (at == run.first ? 0 : 1);
         float* po = p.partials + (int64_t)part * COLS * (D + 2);
@@ -781,17 +816,17 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
                 if (col >= cols) continue;
                 auto dim = [&](int k) { return lane_dim<C::seg>(r, k); };
+                const Average av(sum, ou[nt][j]);
+                auto four = [&](int k) { return make_float4(av(o[nt][k][j]), av(o[nt][k][2 + j]), av(o[nt][k + 1][j]), av(o[nt][k + 1][2 + j])); };
                 if (!complete) {
 #pragma unroll
-                    for (int k = 0; k < KS; k += 2)
-                        *reinterpret_cast<float4*>(po + col * D + dim(k)) = make_float4(o[nt][k][j], o[nt][k][2 + j], o[nt][k + 1][j], o[nt][k + 1][2 + j]);
+                    for (int k = 0; k < KS; k += 2) *reinterpret_cast<float4*>(po + col * D + dim(k)) = four(k);
                     if (r == 0) *reinterpret_cast<float2*>(po + COLS * D + 2 * col) = make_float2(m[nt][j], sum);
                 } else {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     uint16_t* out = p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1];
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
-                        const float4 v = make_float4(o[nt][k][j] * inv, o[nt][k][2 + j] * inv, o[nt][k + 1][j] * inv, o[nt][k + 1][2 + j] * inv);
+                        const float4 v = four(k);
                         uint2 w = q_bf16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w)) : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
                         if (sum == 0.f) w = make_uint2(0, 0);
                         *reinterpret_cast<uint2*>(out + dim(k)) = w;
@@ -815,13 +850,15 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 // the result of a sequence without keys.  The parts are in L2, so latency is its cost: a group of
 // D / 4 lanes takes every stride-th part, kAhead of them loaded at a time.
 
+// O is the average of the keys so far, so that no sum of large values leaves fp32.
 struct Joined {
     float M, L;
     float4 O;
 };
 __device__ __forceinline__ Joined join(const Joined& a, const Joined& b) {
-    const float M = fmaxf(a.M, b.M), fa = ex2_approx(a.M - M), fb = ex2_approx(b.M - M);
-    return {M, a.L * fa + b.L * fb, make_float4(a.O.x * fa + b.O.x * fb, a.O.y * fa + b.O.y * fb, a.O.z * fa + b.O.z * fb, a.O.w * fa + b.O.w * fb)};
+    const float M = fmaxf(a.M, b.M), la = a.L * ex2_approx(a.M - M), lb = b.L * ex2_approx(b.M - M), L = la + lb;
+    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), fa = la * inv, fb = lb * inv;
+    return {M, L, make_float4(a.O.x * fa + b.O.x * fb, a.O.y * fa + b.O.y * fb, a.O.z * fa + b.O.z * fb, a.O.w * fa + b.O.w * fb)};
 }
 
 // A query head: its parts, the first one's slot (the others are the first slots of the following
@@ -863,12 +900,18 @@ __device__ __forceinline__ Joined join_parts(const CacheDecodeParams& p, const M
         float M = r.M;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) M = fmaxf(M, ml[i].x);
-        const float a = ex2_approx(r.M - M);
-        r = {M, r.L * a, make_float4(r.O.x * a, r.O.y * a, r.O.z * a, r.O.w * a)};
+        float a = r.L * ex2_approx(r.M - M), L = a;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const float f = ex2_approx(ml[i].x - M);
-            r.L = fmaf(ml[i].y, f, r.L);
+            ml[i].y *= ex2_approx(ml[i].x - M);
+            L += ml[i].y;
+        }
+        const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+        a *= inv;
+        r = {M, L, make_float4(r.O.x * a, r.O.y * a, r.O.z * a, r.O.w * a)};
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float f = ml[i].y * inv;
             r.O = make_float4(fmaf(v[i].x, f, r.O.x), fmaf(v[i].y, f, r.O.y), fmaf(v[i].z, f, r.O.z), fmaf(v[i].w, f, r.O.w));
         }
     }
@@ -893,9 +936,7 @@ __device__ __forceinline__ Joined join_warp(Joined r) {
 }
 
 __device__ __forceinline__ void write_joined(const CacheDecodeParams& p, bool q_bf16, const MergeHead& m, const Joined& r, int d) {
-    const float inv = r.L == 0.f ? 0.f : 1.f / r.L;
-    uint2 w = q_bf16 ? make_uint2(pack2<true>(r.O.x * inv, r.O.y * inv), pack2<true>(r.O.z * inv, r.O.w * inv))
-                     : make_uint2(pack2<false>(r.O.x * inv, r.O.y * inv), pack2<false>(r.O.z * inv, r.O.w * inv));
+    uint2 w = q_bf16 ? make_uint2(pack2<true>(r.O.x, r.O.y), pack2<true>(r.O.z, r.O.w)) : make_uint2(pack2<false>(r.O.x, r.O.y), pack2<false>(r.O.z, r.O.w));
     if (r.L == 0.f) w = make_uint2(0, 0);
     *reinterpret_cast<uint2*>(p.out + m.b * p.out_stride[0] + (int64_t)m.hq * p.out_stride[1] + d) = w;
     if (d == 0 && p.lse) p.lse[(int64_t)m.b * p.HQ + m.hq] = r.L == 0.f ? -INFINITY : (r.M + log2f(r.L)) * kCdLn2;

@@ -78,7 +78,7 @@ struct CacheDecodeParams {
     void* workspace;
     // Set by launch_cache_decode.
     int2* heads;                  // [B][H][column blocks] parts and the first one's slot
-    float* partials;              // slots of O [cols][D], then (m, l) [cols]
+    float* partials;              // slots of averages [cols][D], then (m, l) [cols]
 };
 int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm);
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st);

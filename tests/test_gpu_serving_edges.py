@@ -125,3 +125,72 @@ def test_decode_largest_bf16_values(lens):
     q[..., 0] = 1.0
     out, lse = fa.decode_attention(q, cache, table, i32(*lens), scale=1.0)
     check_decode(q, out, lse, *rows64(cache, table, lens), lens, scale=1.0)
+
+
+# ---------------------------------------------------------------- row scales over the range of fp32
+
+def scaled_cache(kind, lens, seed, k_log2, v_log2):
+    """Pages of 16 for one head; key j's rows have scales 2^k_log2[j] / 64 and 2^v_log2[j] / 64."""
+    cache, table, _, _ = random_cache(kind, lens, 16, 1, 64, seed=seed, garbage=False)
+    vs = []
+    for b, n in enumerate(lens):
+        at = torch.arange(n, device="cuda")
+        pg, rw = table[b].long()[at // 16], at % 16
+        for sc, e in ((cache.k_scale, k_log2), (cache.v_scale, v_log2)):
+            sc[pg, 0, rw] = torch.exp2(torch.as_tensor(e, dtype=torch.float32, device="cuda").expand(max(lens))[:n] - 6)
+        vs.append(np64(cache.v_scale[pg, 0, rw])[None])
+    return cache, table, vs
+
+
+def check_scaled(q, out, lse, cache, table, lens, kind, vs, scale=None):
+    K, V = rows64(cache, table, lens)
+    for b in range(len(lens)):
+        check_decode(q[b:b + 1], out[b:b + 1], lse[b:b + 1], K[b:b + 1], V[b:b + 1], lens[b:b + 1], scale=scale, kind=kind,
+                     vscale=vs[b])
+
+
+SPREAD = pytest.mark.parametrize("lens", [[300, 500], MANY], ids=["narrow", "split"])
+
+
+@SPREAD
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+@pytest.mark.parametrize("e", [-120, -100, -60, 0, 60, 108, 119, 125])
+def test_decode_value_scales_of_any_size(kind, lens, e):
+    # One key at the top, the others 2^-15 of it: lse does not depend on the values, and the result
+    # scales with them.
+    fa = fa_module()
+    cache, table, vs = scaled_cache(kind, lens, 7, 0.0, float(e))
+    cache.k.view(torch.uint8).zero_()
+    for b, n in enumerate(lens):
+        at = 17 * b % n
+        cache.k[table[b, at // 16].item(), 0, at % 16, 0] = torch.tensor(64.0).to(cache.dtype)
+    q = torch.zeros(len(lens), 3, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 10.4375
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens), scale=1.0)
+    check_scaled(q, out, lse, cache, table, lens, kind, vs, 1.0)
+    assert out.float().abs().amax((1, 2, 3)).min() > 0
+
+
+@SPREAD
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+@pytest.mark.parametrize("lo, hi", [(-120, 110), (90, 125), (-120, -80), (-40, 40)])
+def test_decode_value_scales_of_all_sizes_together(kind, lens, lo, hi):
+    fa = fa_module()
+    e = torch.randint(lo, hi + 1, (max(lens),), generator=torch.Generator().manual_seed(hi)).float()
+    cache, table, vs = scaled_cache(kind, lens, 8, 0.0, e)
+    q = rand((len(lens), 4, 1, 64), seed=5, scale=2.0)
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    check_scaled(q, out, lse, cache, table, lens, kind, vs)
+
+
+@SPREAD
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+def test_decode_zero_scales_beside_others(kind, lens):
+    # Scales of 0, as fresh pools hold them, among ordinary and tiny ones: their rows are zeros.
+    fa = fa_module()
+    e = torch.zeros(max(lens))
+    e[::3], e[1::3], e[:64] = -math.inf, -110.0, -math.inf
+    cache, table, vs = scaled_cache(kind, lens, 9, 0.0, e)
+    q = rand((len(lens), 4, 1, 64), seed=6, scale=3.0)
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    check_scaled(q, out, lse, cache, table, lens, kind, [np.maximum(v, 2.0 ** -116) for v in vs])
