@@ -194,3 +194,16 @@ def test_decode_zero_scales_beside_others(kind, lens):
     q = rand((len(lens), 4, 1, 64), seed=6, scale=3.0)
     out, lse = fa.decode_attention(q, cache, table, i32(*lens))
     check_scaled(q, out, lse, cache, table, lens, kind, [np.maximum(v, 2.0 ** -116) for v in vs])
+
+
+@SPREAD
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+@pytest.mark.parametrize("e", [-100, -30, 60, 100, 112])
+def test_decode_key_scales_of_any_size(kind, lens, e):
+    # Large keys under a small query: the scores are ordinary numbers.
+    fa = fa_module()
+    cache, table, vs = scaled_cache(kind, lens, 10, float(e), 0.0)
+    q = (rand((len(lens), 4, 1, 64), torch.float32, 7) * 2.0 ** -min(e, 100)).to(torch.bfloat16)
+    scale = 2.0 ** (min(e, 100) - e) / 8.0
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens), scale=scale)
+    check_scaled(q, out, lse, cache, table, lens, kind, vs, scale)
