@@ -152,10 +152,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 __device__ __forceinline__ float power_of_two(float k) { return __uint_as_float((uint32_t)((int)k + 127) << 23); }
 __device__ __forceinline__ float exponent_of(float u) { return (float)((int)(__float_as_uint(u) >> 23) - 127); }
 
-// a with its magnitude at most that of the largest finite number.
+// a with its magnitude at most that of the largest finite number; NaN stays NaN.
 __device__ __forceinline__ float finite(float a) {
     float d;
-    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(FLT_MAX));
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(FLT_MAX));
     return d;
 }
 

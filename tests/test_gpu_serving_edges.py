@@ -207,3 +207,24 @@ def test_decode_key_scales_of_any_size(kind, lens, e):
     scale = 2.0 ** (min(e, 100) - e) / 8.0
     out, lse = fa.decode_attention(q, cache, table, i32(*lens), scale=scale)
     check_scaled(q, out, lse, cache, table, lens, kind, vs, scale)
+
+
+@pytest.mark.parametrize("lens", [[300, 60], [3000, 60]], ids=["narrow", "wide"])
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_decode_rows_that_held_no_numbers(kind, lens, late, zeros):
+    # A value row whose scale is NaN (as one written with a NaN or an infinity has, beside codes 0)
+    # makes its head's outputs NaN, but not lse.
+    fa = fa_module()
+    cache, table, _, _ = random_cache(kind, lens, 16, 2, 64, seed=4, garbage=False)
+    q = rand((2, 6, 1, 64), seed=3)
+    clean, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    at = lens[0] - 2 if late else 0
+    page = table[0, at // 16].item()
+    cache.v_scale[page, 1, at % 16] = math.nan
+    if zeros:
+        cache.v.view(torch.uint8)[page, 1, at % 16] = 0
+    out, lse2 = fa.decode_attention(q, cache, table, i32(*lens))
+    assert torch.isnan(out[0, 3:]).all() and torch.isfinite(out[0, :3]).all()
+    assert torch.equal(out[1], clean[1]) and torch.equal(lse2, lse)
