@@ -631,6 +631,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 }
                 // Scores in log2 units; x[2 i + j]: key r + 8 i, column 2c + j.  The key's scale meets
                 // the column's factor first: the product of codes and scaled-up q alone may leave fp32.
+                // (Where their own product leaves it, it counts as the largest number: a sum of 0 stays 0.)
                 float kscale[2] = {1.f, 1.f};
                 if constexpr (C::k8) {
                     const uint4 s4 = lds128(su + C::kbytes + C::vbytes + r * 16);
@@ -643,7 +644,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     for (int i = 0; i < 4; ++i) {
                         float s = acc[nt][0][i];
                         if constexpr (CHAINS == 2) s += acc[nt][1][i];
-                        x[u][nt][i] = s * (C::k8 ? kscale[i >> 1] * cs[nt][i & 1] : cs[nt][i & 1]);
+                        x[u][nt][i] = s * (C::k8 ? finite(kscale[i >> 1] * cs[nt][i & 1]) : cs[nt][i & 1]);
                     }
                 const int key = (t + u) * kTileKeys + r;
                 if (p.score_kind != 0) {

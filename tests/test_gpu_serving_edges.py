@@ -228,3 +228,17 @@ def test_decode_rows_that_held_no_numbers(kind, lens, late, zeros):
     out, lse2 = fa.decode_attention(q, cache, table, i32(*lens))
     assert torch.isnan(out[0, 3:]).all() and torch.isfinite(out[0, :3]).all()
     assert torch.equal(out[1], clean[1]) and torch.equal(lse2, lse)
+
+
+@SPREAD
+@pytest.mark.parametrize("kind", ["s8", "e4m3"])
+def test_decode_scores_of_zero_under_large_factors(kind, lens):
+    # Queries and key scales whose product leaves fp32, met by codes of zero: the scores are zero.
+    fa = fa_module()
+    cache, table, vs = scaled_cache(kind, lens, 11, 100.0, 0.0)
+    cache.k.view(torch.uint8)[..., :32] = 0
+    q = torch.zeros(len(lens), 3, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., :32] = 2.0 ** 120
+    out, lse = fa.decode_attention(q, cache, table, i32(*lens))
+    q.zero_()
+    check_scaled(q, out, lse, cache, table, lens, kind, vs)
