@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const __grid_
     }
 }
 
-// Rows start .. start + S - 1 of each sequence; those past its length are zero.
+// Rows start .. start + S - 1 of each sequence; those past its length, or before position 0, are zero.
 template <int DT, int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
     constexpr int LPR = D / 8;
@@ -251,6 +251,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const __grid_co
             *reinterpret_cast<uint4*>(p.out[w] + b * p.rs[w][0] + h * p.rs[w][1] + (int64_t)s * p.rs[w][2] + sub * 8) = r;
         }
     }
+    // A length or start that no page could hold is recorded even where it touches no page.
+    if (blockIdx.x == 0 && blockIdx.y == 0 && ((unsigned)len > (unsigned)p.c.capacity || (int)start < 0)) g_cache_rows_status = 2;
 }
 
 template <int DT, int D, bool BF16>

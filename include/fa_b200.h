@@ -438,8 +438,8 @@ typedef struct fa_kv_cache {
  *                (b, j) is the page of tokens j * page_size .. of sequence b.  Only the entries of
  *                tokens that a call touches are read.
  *   A page index outside [0, n_pages), a position outside [0, table_width * page_size) or a length
- *   outside [0, table_width * page_size] is skipped (decode: clamped) and recorded:
- *   fa_cache_status then returns FA_ERR_INVALID_ARG.
+ *   outside [0, table_width * page_size] is skipped (decode and read: lengths are clamped) and
+ *   recorded: fa_cache_status then returns FA_ERR_INVALID_ARG.
  *   Two rows of one call must not go to the same place of the cache.
  *   All of them, and fa_rotary, may be captured into a CUDA graph: what changes from replay to
  *   replay (positions, lengths, tables, rows) is device data, and nothing is kept between calls.
@@ -459,7 +459,8 @@ fa_status_t fa_cache_append(const fa_tensor_t* k, const fa_tensor_t* v, const fa
 /*
  * fa_cache_read -- positions start[b] .. start[b] + S - 1 (start NULL: from 0) of each sequence
  * into k_out and v_out (B, H, S, D), fp16 or bf16 (a 16-bit cache's own dtype).  Positions at or
- * past kv_lens[b] (device int32 [B]) come out as zeros, so the result can be attended to as it is.
+ * past kv_lens[b] (device int32 [B]) come out as zeros, so the result can be attended to as it is,
+ * and so do those before position 0, which a negative start[b] asks for and which is recorded.
  */
 fa_status_t fa_cache_read(const fa_kv_cache_t* cache, const int32_t* page_table,
                           int64_t table_stride, int64_t table_width, const int32_t* start,

@@ -242,3 +242,31 @@ def test_decode_scores_of_zero_under_large_factors(kind, lens):
     out, lse = fa.decode_attention(q, cache, table, i32(*lens))
     q.zero_()
     check_scaled(q, out, lse, cache, table, lens, kind, vs)
+
+
+# ---------------------------------------------------------------- reads out of range
+
+@pytest.mark.parametrize("kind", ["s8", "bf16"])
+def test_read_records_lengths_and_starts_out_of_range(kind):
+    # Each the only fault of its call; what is in range is read all the same.
+    fa = fa_module()
+    cache = make_cache(kind, 4, 2, 16, 64)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    x = rand((2, 2, 32, 64), seed=1)
+    fa.cache_append(cache, x, x, table, i32(0, 0))
+    whole, _ = fa.cache_read(cache, table, i32(32, 32), 32)
+    assert fa.cache_status() == fa.FA_OK
+    bad = fa.FA_ERR_INVALID_ARG
+    k, _ = fa.cache_read(cache, table, i32(20, -1), 8)
+    assert fa.cache_status() == bad and torch.equal(k[0], whole[0, :, :8]) and not k[1].any()
+    k, _ = fa.cache_read(cache, table, i32(33, 20), 8)
+    assert fa.cache_status() == bad and torch.equal(k, whole[:, :, :8])
+    k, v = fa.cache_read(cache, table, i32(33, 20), 40)
+    assert fa.cache_status() == bad and torch.equal(k[0, :, :32], whole[0]) and not v[0, :, 32:].any()
+    k, _ = fa.cache_read(cache, table, i32(20, 20), 8, start=i32(0, -2))
+    assert fa.cache_status() == bad and torch.equal(k[0], whole[0, :, :8])
+    assert not k[1, :, :2].any() and torch.equal(k[1, :, 2:], whole[1, :, :6])
+    k, _ = fa.cache_read(cache, table, i32(20, 20), 8, start=i32(0, -100))
+    assert fa.cache_status() == bad and not k[1].any()
+    k, _ = fa.cache_read(cache, table, i32(0, 32), 8, start=i32(50, 40))         # past the length: zeros, no fault
+    assert fa.cache_status() == fa.FA_OK and not k.any()
