@@ -33,7 +33,8 @@ __device__ __forceinline__ float2 rotary_cos_sin(double freq, int64_t pos, float
     double turns = freq * 0.15915494309189533577;      // radians to turns
     turns -= floor(turns);
     const uint64_t fixed = (uint64_t)(turns * 18446744073709551616.0) * (uint64_t)pos;
-    const float x = (float)(int32_t)(fixed >> 32) * 4.656612873077393e-10f;   // half turns, [-1, 1)
+    float x = (float)(int32_t)(fixed >> 32) * 4.656612873077393e-10f;   // half turns, [-1, 1)
+    if (!isfinite(freq)) x = __int_as_float(0x7fc00000);
     float s, c;
     sincospif(x, &s, &c);
     return make_float2(c * factor, (inverse ? -s : s) * factor);

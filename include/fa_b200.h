@@ -394,7 +394,8 @@ fa_status_t fa_rotary_frequencies(int32_t rot_dim, double base, const fa_rotary_
  *   q            (B, Hq, S, D); k (B, Hk, S, D) of the same dtype, or NULL for q alone
  *   positions    device int32 [B][position_stride], entry (b, s); position_stride 0 shares one row
  *                among all sequences; NULL: position0 + s
- *   frequencies  device double[rot_dim / 2], radians a position
+ *   frequencies  device double[rot_dim / 2], radians a position; a pair whose frequency is no finite
+ *                number comes out as NaN
  *   rot_dim      even, 2 .. D
  *   q_out, k_out shapes and dtype of q and k, caller-owned; may be q and k themselves with the
  *                same strides, otherwise must not overlap the inputs.  k_out is NULL iff k is

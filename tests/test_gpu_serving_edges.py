@@ -270,3 +270,24 @@ def test_read_records_lengths_and_starts_out_of_range(kind):
     assert fa.cache_status() == bad and not k[1].any()
     k, _ = fa.cache_read(cache, table, i32(0, 32), 8, start=i32(50, 40))         # past the length: zeros, no fault
     assert fa.cache_status() == fa.FA_OK and not k.any()
+
+
+# ---------------------------------------------------------------- frequencies
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [64, 24, 26])
+def test_rotary_frequencies_that_are_no_numbers(inter, rot):
+    # Their pairs are NaN at every position, as cos and sin of a product with them are; others stay.
+    fa = fa_module()
+    f = fa.rotary_frequencies(rot)
+    f[1], f[4], f[rot // 2 - 1] = math.nan, math.inf, -math.inf
+    x = rand((2, 3, 9, 64), seed=1)
+    pos = torch.arange(9, device="cuda", dtype=torch.int32)
+    y, _ = fa.rotary(x, None, pos, f, interleaved=inter)
+    bad = ~torch.isfinite(f)
+    at = torch.nonzero(bad).flatten().tolist()
+    hit = sorted(2 * i for i in at) + sorted(2 * i + 1 for i in at) if inter else at + [i + rot // 2 for i in at]
+    assert torch.isnan(y[..., hit]).all()
+    f[bad] = 0.0
+    y[..., hit] = x[..., hit]
+    check_rotary(x, y, np.tile(np64(pos), (2, 1)), f, inter, 1.0)
