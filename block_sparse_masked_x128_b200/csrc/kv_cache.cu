@@ -292,17 +292,6 @@ cudaError_t launch_cache_read(const CacheRowsParams& p, int dtype, int D, bool b
     return launch_any(p, dtype, D, bf16, false, st);
 }
 
-cudaError_t cache_rows_status(cudaStream_t st, int32_t* out) {
-    void* addr = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&addr, g_cache_rows_status);
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyAsync(out, addr, 4, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && *out != 0) {
-        e = cudaMemsetAsync(addr, 0, 4, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    return e;
-}
+cudaError_t cache_rows_status_word(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_cache_rows_status); }
 
 }  // namespace fa

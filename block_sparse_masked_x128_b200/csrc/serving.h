@@ -61,7 +61,7 @@ struct CacheRowsParams {
 };
 cudaError_t launch_cache_append(const CacheRowsParams& p, int dtype, int D, bool bf16, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRowsParams& p, int dtype, int D, bool bf16, cudaStream_t st);
-cudaError_t cache_rows_status(cudaStream_t st, int32_t* out);
+cudaError_t cache_rows_status_word(int32_t** word);      // on the current device
 
 struct CacheDecodeParams {
     CacheView c;
@@ -82,7 +82,7 @@ struct CacheDecodeParams {
 };
 int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm);
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st);
-cudaError_t cache_decode_status(cudaStream_t st, int32_t* out);
+cudaError_t cache_decode_status_word(int32_t** word);
 
 #ifdef __CUDACC__
 // The kernels of these operators are short and follow one another: each is launched so that it may

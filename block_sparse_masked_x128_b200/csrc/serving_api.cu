@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -129,6 +130,24 @@ fa_status_t rows_match_cache(const fa_tensor_t* k, const fa_kv_cache_t* c) {
         return fail(FA_ERR_INVALID_ARG, "a 16-bit cache takes and gives its own dtype");
     if (k->S > 0x7fffffffLL - 1024) return fail(FA_ERR_UNSUPPORTED, "more than 2^31 - 1024 rows a sequence");
     return FA_OK;
+}
+
+// Reads and clears the status words in one act each, so that what a kernel on another stream records
+// meanwhile is either taken here or left for the next look.
+__device__ int32_t g_status_taken;
+__global__ void take_status_kernel(int32_t* rows, int32_t* decode) { g_status_taken = atomicExch(rows, 0) | atomicExch(decode, 0); }
+
+cudaError_t take_status(cudaStream_t st, int32_t* out) {
+    int32_t *rows = nullptr, *decode = nullptr;
+    cudaError_t e = fa::cache_rows_status_word(&rows);
+    if (e == cudaSuccess) e = fa::cache_decode_status_word(&decode);
+    if (e != cudaSuccess) return e;
+    static std::mutex mutex;        // one look at a time: g_status_taken is one word a device
+    std::lock_guard<std::mutex> lock(mutex);
+    take_status_kernel<<<1, 1, 0, st>>>(rows, decode);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(out, g_status_taken, sizeof(*out), 0, cudaMemcpyDeviceToHost, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
 fa_status_t current_device(int* dev) {
@@ -380,11 +399,10 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
 }
 
 fa_status_t fa_cache_status(void* stream) {
-    int32_t rows = 0, decode = 0;
-    cudaError_t e = fa::cache_rows_status(static_cast<cudaStream_t>(stream), &rows);
-    if (e == cudaSuccess) e = fa::cache_decode_status(static_cast<cudaStream_t>(stream), &decode);
+    int32_t taken = 0;
+    const cudaError_t e = take_status(static_cast<cudaStream_t>(stream), &taken);
     if (e != cudaSuccess) return cuda_fail(e, "reading the cache status words");
-    if (rows != 0 || decode != 0)
+    if (taken != 0)
         return fail(FA_ERR_INVALID_ARG, "a page index, position or length was out of range");
     return fa::record_ok();
 }

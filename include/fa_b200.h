@@ -492,8 +492,10 @@ fa_status_t fa_decode(const fa_tensor_t* q, const fa_kv_cache_t* cache, const in
                       float scale, fa_tensor_t* out, float* lse, void* workspace,
                       size_t workspace_bytes, void* stream);
 
-/* Synchronise `stream`, read and clear the status words of the calls on caches on the current
- * device: FA_OK, FA_ERR_INVALID_ARG (a page, position or length was out of range), FA_ERR_CUDA. */
+/* Synchronise `stream`, read and clear the status of the calls on caches on the current device:
+ * FA_OK, FA_ERR_INVALID_ARG (a page, position or length was out of range), FA_ERR_CUDA.  All caches
+ * and streams of a device share it: a look takes what the calls before it on `stream`, and any others
+ * that have run by then, recorded.  Not for use while `stream` is captured. */
 fa_status_t fa_cache_status(void* stream);
 
 /* Fill `info` with the mask's extents and device pointers.  FA_ERR_INVALID_ARG on NULL. */

@@ -291,3 +291,62 @@ def test_rotary_frequencies_that_are_no_numbers(inter, rot):
     f[bad] = 0.0
     y[..., hit] = x[..., hit]
     check_rotary(x, y, np.tile(np64(pos), (2, 1)), f, inter, 1.0)
+
+
+# ---------------------------------------------------------------- the status
+
+def test_status_is_shared_by_streams_and_taken_once():
+    # Faults of the rows' calls and of decode, on two streams; each is seen by exactly one look, and what
+    # is recorded between two looks is the second one's.
+    fa = fa_module()
+    cache, table, _, _ = random_cache("s8", [20, 20], 16, 2, 64)
+    q, n, long = rand((2, 4, 1, 64)), i32(20, 20), i32(20, 5000)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    calls = (lambda: fa.decode_attention(q, cache, table, long), lambda: fa.cache_read(cache, table, long, 4))
+    for first in range(2):
+        for both in (False, True):
+            with torch.cuda.stream(streams[first]):
+                calls[first]()
+                if both:
+                    calls[1 - first]()
+            torch.cuda.synchronize()
+            assert fa.cache_status(streams[1 - first]) == fa.FA_ERR_INVALID_ARG
+            assert fa.cache_status(streams[first]) == fa.FA_OK
+            with torch.cuda.stream(streams[first]):
+                fa.decode_attention(q, cache, table, n)
+            assert fa.cache_status(streams[first]) == fa.FA_OK
+
+
+def test_status_loses_nothing_under_concurrent_looks():
+    # One thread polls one stream while another records a fault on a second stream and waits for it:
+    # every fault has to be seen by a look that ends after it.
+    import threading
+    fa = fa_module()
+    cache, table, _, _ = random_cache("s8", [20, 20], 16, 2, 64)
+    long = i32(20, 5000)
+    side, poll = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen, stop = [0], threading.Event()
+
+    def look():
+        while not stop.is_set():
+            seen[0] += fa.cache_status(poll) != fa.FA_OK
+
+    thread = threading.Thread(target=look)
+    thread.start()
+    try:
+        for _ in range(200):
+            before = seen[0]
+            with torch.cuda.stream(side):
+                fa.cache_read(cache, table, long, 4)
+            side.synchronize()
+            for _ in range(20000):
+                if seen[0] > before:
+                    break
+                stop.wait(0.0005)
+            assert seen[0] > before
+    finally:
+        stop.set()
+        thread.join()
+    assert fa.cache_status() == fa.FA_OK
