@@ -4,7 +4,8 @@
 
 (Run it as a file, not as a package module: importing the package loads the library.)
 
-Beside it goes _lib/fa_b200_torch.so, the host path of the serving calls (g++ against torch's headers).
+Beside it goes _lib/fa_b200_torch.so, the host path of the Python serving calls (g++ against torch's
+headers; left out where torch is not installed: the library does not need it).
 Each .cu file is compiled to an object in parallel (nvcc cross-compiles for sm_100a without
 a GPU), then linked into one shared library exporting the C ABI of include/fa_b200.h.
 Objects are rebuilt only when a source or header is newer.  `--ptxas-info` prints the
@@ -12,13 +13,13 @@ registers and shared memory of every kernel (nvcc -Xptxas -v).
 """
 from __future__ import annotations
 
-
 import argparse
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -72,14 +73,17 @@ def _compile(src: str, flags: list, force: bool, build_dir: str = BUILD) -> tupl
     return obj, r.stdout + r.stderr
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile csrc/binding.cpp, the Python extension that takes torch tensors to the C ABI."""
-    src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "fa_b200.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+def build_binding(force: bool = False) -> Optional[str]:
+    """Compile csrc/binding.cpp, the Python extension that takes torch tensors to the C ABI.  None where
+    torch is not installed."""
+    try:
+        import torch
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        return None
     import sysconfig
-    import torch
+    src = os.path.join(CSRC, "binding.cpp")
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     os.makedirs(LIBDIR, exist_ok=True)
@@ -89,6 +93,9 @@ def build_binding(force: bool = False) -> str:
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), src, "-o", BINDING,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "fa_b200.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -108,7 +115,6 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(build_binding, force)
         results = list(ex.map(lambda s: _compile(s, flags, force or ptxas_info, build_dir), SOURCES))
-        binding.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_info:
         for _, log in results:
@@ -120,6 +126,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    # Last, so that whatever the binding lacks, the library is there.
+    if binding.result() is None and verbose:
+        print("torch is not installed: fa_b200_torch.so (the Python serving calls) is left out")
     return lib
 
 
