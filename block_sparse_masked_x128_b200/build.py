@@ -86,6 +86,7 @@ def build_binding(force: bool = False) -> Optional[str]:
     src = os.path.join(CSRC, "binding.cpp")
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
@@ -93,12 +94,20 @@ def build_binding(force: bool = False) -> Optional[str]:
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"), src, "-o", BINDING,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    # Current: newer than its sources and made by this command (wherever the tree lies) against this
+    # torch and Python.
+    made = "\n".join([*cmd, torch.__version__, str(torch.version.git_version), sys.version]).replace(ROOT, "")
+    stamp = os.path.join(BUILD, "fa_b200_torch.made")
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "fa_b200.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made:
+                return BINDING
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made)
     return BINDING
 
 

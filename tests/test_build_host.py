@@ -1,9 +1,11 @@
-"""The build script: the library needs nvcc alone."""
+"""The build script: the library needs nvcc alone, and the host path of the Python serving calls is
+rebuilt when what it was made against changes."""
 import builtins
 import os
 import sys
 
 import pytest
+import torch
 
 from test_abi import _build_module
 
@@ -57,3 +59,17 @@ def test_library_is_linked_when_the_binding_fails(build):
     with pytest.raises(RuntimeError, match="binding"):
         build.build()
     assert os.path.exists(build.LIB)
+
+
+def test_binding_is_rebuilt_for_another_torch(build, monkeypatch):
+    assert build.build_binding() == build.BINDING and build.ran == ["g++"]
+    build.build_binding()
+    assert build.ran == ["g++"]                          # current
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    build.build_binding()
+    assert build.ran == ["g++"] * 2
+    build.build_binding()
+    assert build.ran == ["g++"] * 2
+    os.utime(build.BINDING, (0, 0))                      # older than its sources
+    build.build_binding()
+    assert build.ran == ["g++"] * 3
