@@ -350,3 +350,60 @@ def test_status_loses_nothing_under_concurrent_looks():
         stop.set()
         thread.join()
     assert fa.cache_status() == fa.FA_OK
+
+
+# ---------------------------------------------------------------- bad pages and lengths where keys are split
+
+@pytest.mark.parametrize("kind, D", [("bf16", 64), ("f16", 128), ("s8", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("B, H, G", [(4, 2, 4), (12, 4, 10), (36, 8, 8)], ids=["few", "more", "many"])
+def test_decode_bad_pages_and_lengths_over_wide_tables(kind, D, B, H, G):
+    # Tables of more than 1024 tokens, so the keys of a head are split over warps and their parts are
+    # joined (in three ways, by the number of heads).  A bad page's keys count for nothing; a run of
+    # bad pages leaves parts, or a whole sequence, without a key; too long a length ends at the table.
+    fa = fa_module()
+    page = 32
+    lens = [1200 + (997 * b) % 1500 for b in range(B)]
+    cache, table, K, V = random_cache(kind, lens, page, H, D, seed=B)
+    width = -(-max(lens) // page)
+    table = table[:, :width].contiguous()
+    g = torch.Generator().manual_seed(B)
+    keep = [np.ones(n, dtype=bool) for n in lens]
+
+    def lose(b, j, index):
+        table[b, j] = index
+        keep[b][j * page:(j + 1) * page] = False
+
+    for b, n in enumerate(lens):
+        pages = -(-n // page)
+        if b % 4 == 1:
+            for j in range(pages):                       # all
+                lose(b, j, -1 - j)
+        elif b % 4 == 2:
+            for j in range(pages // 5, pages // 2):      # one run
+                lose(b, j, cache.n_pages)
+        elif b % 4 == 3:
+            for j in torch.randperm(pages, generator=g)[:pages // 3].tolist() + [pages - 1]:
+                lose(b, j, 2 ** 30 + j)
+    said = list(lens)
+    said[0] = width * page + 1                           # longer than the table: all that it maps
+    long = width * page
+    table[0] = table[0].clamp(0, cache.n_pages - 1)
+    for w, into in ((0, K), (1, V)):
+        into[0] = gather64(cache, table, 0, long, w)
+    dead = np.isnan(K[0]).any((0, 2)) | np.isnan(V[0]).any((0, 2))      # pool rows that hold no numbers
+    for j in range(long // page):
+        if dead[j * page:(j + 1) * page].any():
+            table[0, j] = -7
+            dead[j * page:(j + 1) * page] = True
+    keep[0] = ~dead
+    said.append(-5)                                      # a sequence of negative length
+    table = torch.cat((table, table[:1]))
+    q = rand((B + 1, H * G, 1, D), TYPES["f16" if kind == "f16" else "bf16"], 5, 1.5)
+    out, lse = fa.decode_attention(q, cache, table, i32(*said))
+    assert fa.cache_status() == fa.FA_ERR_INVALID_ARG and fa.cache_status() == fa.FA_OK
+    rows = [[x[b][:, keep[b]] for b in range(B)] for x in (K, V)]
+    check_decode(q[:B], out[:B], lse[:B], *rows, [int(k.sum()) for k in keep], kind=kind)
+    assert not out[B].any() and torch.isneginf(lse[B]).all()
+    said = [0 if b == 0 or not keep[b].all() else n for b, n in enumerate(lens)] + [0]
+    fa.decode_attention(q, cache, table, i32(*said))
+    assert fa.cache_status() == fa.FA_OK
