@@ -31,8 +31,8 @@
 //   Softmax    l sums 2^(x_j - m) in fp32, and O sums w_j v_j with w_j = 2^(x_j - m); over 8-bit
 //              caches w_j code_j with w_j = 2^(x_j - m) (vscale_j u), u a power of two that takes
 //              the largest weight near 1, so neither sum depends on the size of the other's terms.
-//              For the product a weight becomes one fp16 number over 8-bit caches, two 16-bit
-//              numbers over 16-bit ones.  m is raised to the largest x_j so far, and u set by the
+//              For the product a weight becomes two 16-bit numbers (bf16 results over 8-bit caches:
+//              one fp16 number).  m is raised to the largest x_j so far, and u set by the
 //              largest x_j + log2 vscale_j, only when a weight exceeds 2^8 (bf16 caches: m to 8
 //              above the largest x_j, when one exceeds 1): most tiles need no reduction over the
 //              lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16 at least) or, in
@@ -288,9 +288,9 @@ struct Average {
 
 // Joins the parts (m, l, average) of the CTA's warps in shared memory (over the rings, which are done
 // with) and writes the result.
-template <int DT, int D, int NT>
+template <int DT, int D, int NT, bool QBF>
 __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8_t* smem, const float (&o)[NT][D / 16][4], const float (&m)[NT][2],
-                                               const float (&unit)[NT][2], const float (&l)[NT][2], int b, int hq0, int cols, bool q_bf16) {
+                                               const float (&unit)[NT][2], const float (&l)[NT][2], int b, int hq0, int cols) {
     using C = CdConfig<DT, D, NT>;
     constexpr int COLS = 8 * NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -349,17 +349,18 @@ __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8
             const float4 v = *reinterpret_cast<const float4*>(so + (w * COLS + col) * C::orow + dim + dim / C::seg * 4);
             s = make_float4(fmaf(v.x, f, s.x), fmaf(v.y, f, s.y), fmaf(v.z, f, s.z), fmaf(v.w, f, s.w));
         }
-        uint2 w = q_bf16 ? make_uint2(pack2<true>(s.x, s.y), pack2<true>(s.z, s.w)) : make_uint2(pack2<false>(s.x, s.y), pack2<false>(s.z, s.w));
+        uint2 w = make_uint2(pack2<QBF>(s.x, s.y), pack2<QBF>(s.z, s.w));
         if (sL[col] == 0.f) w = make_uint2(0, 0);
         *reinterpret_cast<uint2*>(p.out + b * p.out_stride[0] + (int64_t)(hq0 + col) * p.out_stride[1] + dim) = w;
     }
 }
 
 // WHOLE: a CTA takes all the keys of a (sequence, kv head, block of columns), its warps every fourth
-// step, and joins its warps' parts itself: one launch, for tables that map few tokens.
-template <int DT, int D, int NT, bool WHOLE>
+// step, and joins its warps' parts itself: one launch, for tables that map few tokens.  QBF: q and the
+// result are bf16.
+template <int DT, int D, int NT, bool WHOLE, bool QBF>
 __global__ void __launch_bounds__(kCdThreads, CdConfig<DT, D, NT>::occ)
-cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
+cache_decode_kernel(const __grid_constant__ CacheDecodeParams p) {
     using C = CdConfig<DT, D, NT>;
     constexpr bool BF16 = DT == FA_DTYPE_BF16;      // type of the products (8-bit: fp16)
     constexpr int KS = D / 16;                      // contraction steps of K q^T, and row tiles of O^T
@@ -552,7 +553,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                     const uint32_t w[2] = {raw[s].x, raw[s].y};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float2 two = q_bf16 ? unpack2<true>(w[i]) : unpack2<false>(w[i]);
+                        const float2 two = unpack2<QBF>(w[i]);
                         f[s][2 * i] = two.x;
                         f[s][2 * i + 1] = two.y;
                         top = max(top, max(__float_as_uint(f[s][2 * i]) & 0x7fffffffu, __float_as_uint(f[s][2 * i + 1]) & 0x7fffffffu));
@@ -731,7 +732,10 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                 // it in bf16 alone put the result's error at 1.3 times that of its own rounding.  A positive
                 // weight's first number is positive (fp16's least, 2^-24, at least; the rest, which may be
                 // negative, makes up for it) and alone meets infinite values, so that they stay infinite.
-                constexpr int PARTS = C::k8 ? 1 : 2;
+                // Over 8-bit caches the second number is for fp16 results (error 3.0e-4 of their norm with one,
+                // 2.07e-4 with two); a bf16 result's own rounding is 8 times that of one number (grouped s8
+                // with two: 32.2 us, with one 31.0).
+                constexpr int PARTS = C::k8 && QBF ? 1 : 2;
                 uint32_t pb[PARTS][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -742,7 +746,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                         auto first = [](float w) { return DT == FA_DTYPE_F16 && w > 0.f ? fmaxf(w, 0x1p-24f) : w; };
                         const uint32_t two = pack2<BF16>(first(w[u][nt][2 * i]), first(w[u][nt][2 * i + 1]));
                         pb[0][nt][i] = transpose8x8(two);
-                        if constexpr (!C::k8) {
+                        if constexpr (PARTS == 2) {
                             const float2 r2 = unpack2<BF16>(two);
                             pb[1][nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i] - r2.x, w[u][nt][2 * i + 1] - r2.y));
                         }
@@ -770,7 +774,9 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
                             const uint32_t a0 = codes_to_half2<DT, 0>(pa), a1 = codes_to_half2<DT, 1>(pa);
                             const uint32_t a2 = codes_to_half2<DT, 0>(pc), a3 = codes_to_half2<DT, 1>(pc);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int k = 0; k < PARTS; ++k) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
                         }
                 } else {
 #pragma unroll
@@ -797,7 +803,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
             slot = slot + 1 == C::stages ? 0 : slot + 1;
         }
         if constexpr (WHOLE) {
-            join_and_write<DT, D, NT>(p, smem, o, m, ou, l, b, hq0, cols, q_bf16);
+            join_and_write<DT, D, NT, QBF>(p, smem, o, m, ou, l, b, hq0, cols);
             return;
         }
         // The part's (m, l, average), or the result.  A worker's first head has slot 2 worker, a later one
@@ -828,7 +834,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p, bool q_bf16) {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2) {
                         const float4 v = four(k);
-                        uint2 w = q_bf16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w)) : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+                        uint2 w = make_uint2(pack2<QBF>(v.x, v.y), pack2<QBF>(v.z, v.w));
                         if (sum == 0.f) w = make_uint2(0, 0);
                         *reinterpret_cast<uint2*>(out + dim(k)) = w;
                     }
@@ -1002,10 +1008,10 @@ int64_t heads_bytes(int64_t B, int64_t HQ, int64_t HK) {
 }
 
 // The kernel, with its shared memory allowed once a device.
-template <int DT, int D, int NT, bool WHOLE>
-cudaError_t launch_kernel(const CacheDecodeParams& p, bool q_bf16, unsigned grid, cudaStream_t st) {
+template <int DT, int D, int NT, bool WHOLE, bool QBF>
+cudaError_t launch_kernel(const CacheDecodeParams& p, unsigned grid, cudaStream_t st) {
     using C = CdConfig<DT, D, NT>;
-    auto kern = cache_decode_kernel<DT, D, NT, WHOLE>;
+    auto kern = cache_decode_kernel<DT, D, NT, WHOLE, QBF>;
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1015,11 +1021,11 @@ cudaError_t launch_kernel(const CacheDecodeParams& p, bool q_bf16, unsigned grid
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    return launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p, q_bf16);
+    return launch_early(kern, dim3(grid), dim3(kCdThreads), C::smem, st, p);
 }
 
-template <int DT, int D, int NT>
-cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t st) {
+template <int DT, int D, int NT, bool QBF>
+cudaError_t launch_split(CacheDecodeParams p, int nsm, cudaStream_t st) {
     using C = CdConfig<DT, D, NT>;
     static_assert(C::occ <= kMaxOcc, "the workspace counts kMaxOcc CTAs an SM");
     const int64_t blocks = (int64_t)p.B * p.c.H * col_blocks(p.group, 8 * NT);
@@ -1029,11 +1035,11 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     // every SM (32 of 500-1000: 20 against 23; with 16 heads in all 14.8 against 11.5).
     const int keys = p.window > 0 ? std::min(p.window, p.c.capacity) : p.c.capacity;
     if (keys <= 512 || (keys <= 1024 && blocks >= nsm))
-        return launch_kernel<DT, D, NT, true>(p, q_bf16, (unsigned)blocks, st);
+        return launch_kernel<DT, D, NT, true, QBF>(p, (unsigned)blocks, st);
     const int grid = nsm * C::occ;
     p.heads = static_cast<int2*>(p.workspace);
     p.partials = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + heads_bytes(p.B, p.HQ, p.c.H));
-    cudaError_t e = launch_kernel<DT, D, NT, false>(p, q_bf16, (unsigned)grid, st);
+    cudaError_t e = launch_kernel<DT, D, NT, false, QBF>(p, (unsigned)grid, st);
     if (e != cudaSuccess) return e;
     const int64_t heads = (int64_t)p.B * p.HQ;
     const int cols = 8 * NT, sub = C::sub;
@@ -1043,10 +1049,10 @@ cudaError_t launch_split(CacheDecodeParams p, bool q_bf16, int nsm, cudaStream_t
     // kv head (whole calls: 1024 heads of 14 parts 30 us with four warps a head, 33 with one; 5824
     // heads of one part 7.5 us by kv heads, 11.8 with four warps a query head).
     if (heads <= nsm)
-        return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, q_bf16, cols, sub);
+        return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, QBF, cols, sub);
     if (heads <= 12 * nsm)
-        return launch_early(cache_decode_merge_head_kernel<D, 1, 4>, dim3((unsigned)heads), dim3(128), 0, st, p, q_bf16, cols, sub);
-    return launch_early(cache_decode_merge_block_kernel<D>, dim3((unsigned)blocks), dim3(kBlockThreads), 0, st, p, q_bf16, cols, sub);
+        return launch_early(cache_decode_merge_head_kernel<D, 1, 4>, dim3((unsigned)heads), dim3(128), 0, st, p, QBF, cols, sub);
+    return launch_early(cache_decode_merge_block_kernel<D>, dim3((unsigned)blocks), dim3(kBlockThreads), 0, st, p, QBF, cols, sub);
 }
 
 }  // namespace
@@ -1056,11 +1062,17 @@ int64_t cache_decode_workspace_bytes(int B, int HQ, int HK, int D, int nsm) {
 }
 
 cudaError_t launch_cache_decode(const CacheDecodeParams& p, int dtype, int D, bool q_bf16, int nsm, cudaStream_t st) {
-#define FA_CD(T, DD)              \
-    if (dtype == T && D == DD)    \
-        return columns(p.group) == 8 ? launch_split<T, DD, 1>(p, q_bf16, nsm, st) : launch_split<T, DD, 2>(p, q_bf16, nsm, st);
-    FA_CD(FA_DTYPE_F16, 64) FA_CD(FA_DTYPE_F16, 128) FA_CD(FA_DTYPE_BF16, 64) FA_CD(FA_DTYPE_BF16, 128)
-    FA_CD(FA_DTYPE_E4M3, 64) FA_CD(FA_DTYPE_E4M3, 128) FA_CD(FA_DTYPE_S8, 64) FA_CD(FA_DTYPE_S8, 128)
+#define FA_CD(T, DD, BB)                        \
+    if (dtype == T && D == DD && q_bf16 == BB)  \
+        return columns(p.group) == 8 ? launch_split<T, DD, 1, BB>(p, nsm, st) : launch_split<T, DD, 2, BB>(p, nsm, st);
+#define FA_CD_D(T, BB) FA_CD(T, 64, BB) FA_CD(T, 128, BB)
+    FA_CD_D(FA_DTYPE_F16, false)
+    FA_CD_D(FA_DTYPE_BF16, true)
+    FA_CD_D(FA_DTYPE_E4M3, false)
+    FA_CD_D(FA_DTYPE_E4M3, true)
+    FA_CD_D(FA_DTYPE_S8, false)
+    FA_CD_D(FA_DTYPE_S8, true)
+#undef FA_CD_D
 #undef FA_CD
     return cudaErrorInvalidValue;
 }
