@@ -512,6 +512,8 @@ def flex_attention(q, k, v, block_mask: BlockMask, *, score_mod: int = FA_SCORE_
                 if need > 0:
                     if workspace is None:
                         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                    elif not workspace.is_contiguous():      # counts bytes that its memory does not hold
+                        raise ValueError("workspace must be a contiguous tensor")
                     ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
             st = _lib.fa_forward_paged(ctypes.byref(fa_tensor(q)), ctypes.byref(fa_tensor(k)),
                                        ctypes.byref(fa_tensor(v)), page_table.data_ptr(),
@@ -554,8 +556,9 @@ def flex_attention_backward(q, k, v, out, lse, dout, block_mask: BlockMask, *,
     nbytes = fa_backward_workspace_bytes(q.shape[0], q.shape[1], q.shape[2])
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif workspace.numel() * workspace.element_size() < nbytes or not workspace.is_cuda:
-        raise ValueError(f"workspace must be a CUDA buffer of at least {nbytes} bytes")
+    elif (workspace.numel() * workspace.element_size() < nbytes or not workspace.is_cuda
+          or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {nbytes} bytes")
     params = FaScoreParams(float(softcap), _check_alibi(alibi_slopes, q))
     with torch.cuda.device(q.device):
         fa_backward(fa_tensor(q), fa_tensor(k), fa_tensor(v), fa_tensor(out), fa_tensor(dout),

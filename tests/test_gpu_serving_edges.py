@@ -45,6 +45,22 @@ def test_decode_refuses_a_workspace_that_is_not_contiguous():
     torch.cuda.synchronize()
 
 
+def test_attention_calls_refuse_a_workspace_that_is_not_contiguous():
+    fa = fa_module()
+    q, k, v = (rand((1, 2, 256, 64), seed=s) for s in range(3))
+    bm = fa.create_block_mask(fa.FA_MASK_CAUSAL, None, None, 256, 256)
+    out, lse = fa.flex_attention(q, k, v, bm)
+    bad = torch.empty(16, dtype=torch.uint8, device="cuda")[:1].expand(1 << 24)
+    with pytest.raises(ValueError, match="workspace"):
+        fa.flex_attention_backward(q, k, v, out, lse, rand(q.shape, seed=3), bm, workspace=bad)
+    pools = [rand((64, 2, 128, 64), seed=s) for s in range(2)]
+    table = torch.arange(64, dtype=torch.int32, device="cuda")[None]
+    one = fa.create_block_mask(fa.FA_MASK_CAUSAL, None, None, 1, 64 * 128)
+    with pytest.raises(ValueError, match="workspace"):
+        fa.flex_attention(q[:, :, :1].contiguous(), *pools, one, page_table=table, workspace=bad)
+    torch.cuda.synchronize()
+
+
 # ---------------------------------------------------------------- infinities in 16-bit caches
 
 @pytest.mark.parametrize("lens", [NARROW, WIDE], ids=["narrow", "wide"])
