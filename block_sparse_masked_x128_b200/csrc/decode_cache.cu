@@ -49,8 +49,6 @@
 #include <atomic>
 #include <cfloat>
 
-#include <cuda_fp16.h>
-
 namespace fa {
 namespace {
 
@@ -122,11 +120,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ float lds_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 
 // D (16 x 8) += A (16 x 16) B (16 x 8), fp32 accumulation.  With r = lane / 4, c = lane % 4: A's
 // registers hold (row r, k 2c 2c+1), (r + 8, same), (r, k 2c+8 2c+9), (r + 8, same); B's (k 2c 2c+1,
@@ -157,12 +150,6 @@ __device__ __forceinline__ float finite(float a) {
     float d;
     asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(FLT_MAX));
     return d;
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return make_float2(__half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))), __half2float(__ushort_as_half((unsigned short)(w >> 16))));
 }
 
 // Two 16-bit values with infinities as the largest finite ones.

@@ -22,8 +22,6 @@
 
 #include <algorithm>
 
-#include <cuda_fp16.h>
-
 namespace fa {
 namespace {
 
@@ -37,13 +35,9 @@ __device__ __forceinline__ void row_unpack(const uint4& r, float (&f)[8]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        } else {
-            f[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xFFFFu)));
-            f[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
-        }
+        const float2 two = unpack2<BF16>(w[i]);
+        f[2 * i] = two.x;
+        f[2 * i + 1] = two.y;
     }
 }
 
@@ -91,8 +85,7 @@ __device__ __forceinline__ uint32_t quantise_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float2 value_e4m3x2(uint32_t codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    return make_float2(__half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu))),
-                       __half2float(__ushort_as_half((unsigned short)(h >> 16))));
+    return unpack2<false>(h);
 }
 
 // The scale of a row from the bits of its largest magnitude.

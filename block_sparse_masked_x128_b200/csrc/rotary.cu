@@ -21,8 +21,6 @@
 
 #include <algorithm>
 
-#include <cuda_fp16.h>
-
 namespace fa {
 namespace {
 
@@ -38,18 +36,6 @@ __device__ __forceinline__ float2 rotary_cos_sin(double freq, int64_t pos, float
     float s, c;
     sincospif(x, &s, &c);
     return make_float2(c * factor, (inverse ? -s : s) * factor);
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 rot_unpack(uint32_t w) {
-    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    return make_float2(__half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))),
-                       __half2float(__ushort_as_half((unsigned short)(w >> 16))));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint16_t rot_round(float v) {
-    return (uint16_t)(pack2<BF16>(v, 0.f) & 0xFFFFu);
 }
 
 // cos and sin (times the factor) of the first `half` pairs of tokens t0 .. t0 + nt - 1 of sequence
@@ -179,7 +165,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(turn + i * rot_cols * 2);
-                        const float2 e = rot_unpack<BF16>(v[k][2 * i]), f = rot_unpack<BF16>(v[k][2 * i + 1]);
+                        const float2 e = unpack2<BF16>(v[k][2 * i]), f = unpack2<BF16>(v[k][2 * i + 1]);
                         if (full || col * W + 2 * i < p.half) v[k][2 * i] = pack2<BF16>(e.x * q.x - e.y * q.y, e.y * q.x + e.x * q.y);
                         if (full || col * W + 2 * i + 1 < p.half) v[k][2 * i + 1] = pack2<BF16>(f.x * q.z - f.y * q.w, f.y * q.z + f.x * q.w);
                     }
@@ -187,7 +173,7 @@ __global__ void __launch_bounds__(kRotThreads, 4) rotary_columns_kernel(const __
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(turn + i * rot_cols * 2);
-                        const float2 x1 = rot_unpack<BF16>(v[k][i]), x2 = rot_unpack<BF16>(v[k][W + i]);
+                        const float2 x1 = unpack2<BF16>(v[k][i]), x2 = unpack2<BF16>(v[k][W + i]);
                         v[k][i] = pack2<BF16>(x1.x * q.x - x2.x * q.y, x1.y * q.z - x2.y * q.w);
                         v[k][W + i] = pack2<BF16>(x2.x * q.x + x1.x * q.y, x2.y * q.z + x1.y * q.w);
                     }
@@ -219,7 +205,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_pairs_kernel(const __grid_
             uint16_t* y = p.y[w] + tile.b * p.ys[w][0] + h * p.ys[w][1] + s * p.ys[w][2];
             if (j < p.half) {
                 const float2 v = cs[t * p.half + j];
-                const float x1 = rot_unpack<BF16>(x[j]).x, x2 = rot_unpack<BF16>(x[j + p.half]).x;
+                const float x1 = unpack2<BF16>(x[j]).x, x2 = unpack2<BF16>(x[j + p.half]).x;
                 const uint32_t u = pack2<BF16>(x1 * v.x - x2 * v.y, x2 * v.x + x1 * v.y);
                 y[j] = (uint16_t)(u & 0xFFFFu);
                 y[j + p.half] = (uint16_t)(u >> 16);

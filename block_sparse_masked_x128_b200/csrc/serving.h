@@ -4,6 +4,10 @@
 
 #include "fa_internal.h"
 
+#ifdef __CUDACC__
+#include <cuda_fp16.h>
+#endif
+
 namespace fa {
 
 // Checks of api.cu that every entry point shares.
@@ -90,8 +94,8 @@ cudaError_t cache_decode_status_word(int32_t** word);
 // (with all the predecessor's writes) before it reads or writes anything.  What overlaps is the
 // launch.  The predecessor may write what they read (positions, lengths, tables, rows) while they
 // are already on the SMs, so they load it as memory that changes, not by __ldg, whose data must stay
-// the same for a kernel's whole life.  A kernel that comes to grid_dependency_release in all its blocks lets its successor
-// start there rather than at its own end.
+// the same for a kernel's whole life.  A kernel that comes to grid_dependency_release in all its
+// blocks lets its successor start there rather than at its own end.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -108,6 +112,13 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, dim3 block, size_
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Two 16-bit values as fp32, the low half first.
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return make_float2(__half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))), __half2float(__ushort_as_half((unsigned short)(w >> 16))));
 }
 
 // The page of position `pos` (32 bits without sign) by a sequence's row of the table, or -1 where
