@@ -269,9 +269,11 @@ __device__ __forceinline__ int lane_dim(int r, int k) {
 // as small as fp32 goes (no key: 0).
 struct Average {
     float inv, unit;
-    __device__ __forceinline__ Average(float l, float u) : inv(l == 0.f ? 0.f : 1.f / l), unit(power_of_two(-exponent_of(u))) {}
     __device__ __forceinline__ float operator()(float o) const { return o * inv * unit; }
 };
+__device__ __forceinline__ Average average(float l, float u) {
+    return {l == 0.f ? 0.f : __fdividef(1.f, l), power_of_two(-exponent_of(u))};
+}
 
 // Joins the parts (m, l, average) of the CTA's warps in shared memory (over the rings, which are done
 // with) and writes the result.
@@ -299,7 +301,7 @@ __device__ __forceinline__ void join_and_write(const CacheDecodeParams& p, uint8
                 sm[warp * COLS + col] = m[nt][j];
                 sl[warp * COLS + col] = sum;
             }
-            const Average av(sum, unit[nt][j]);
+            const Average av = average(sum, unit[nt][j]);
             float* row = so + (warp * COLS + col) * C::orow;
 #pragma unroll
             for (int k = 0; k < D / 16; k += 2) {
@@ -810,7 +812,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p) {
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
                 if (col >= cols) continue;
                 auto dim = [&](int k) { return lane_dim<C::seg>(r, k); };
-                const Average av(sum, ou[nt][j]);
+                const Average av = average(sum, ou[nt][j]);
                 auto four = [&](int k) { return make_float4(av(o[nt][k][j]), av(o[nt][k][2 + j]), av(o[nt][k + 1][j]), av(o[nt][k + 1][2 + j])); };
                 if (!complete) {
 #pragma unroll
@@ -849,10 +851,20 @@ struct Joined {
     float M, L;
     float4 O;
 };
-__device__ __forceinline__ Joined join(const Joined& a, const Joined& b) {
-    const float M = fmaxf(a.M, b.M), la = a.L * ex2_approx(a.M - M), lb = b.L * ex2_approx(b.M - M), L = la + lb;
-    const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), fa = la * inv, fb = lb * inv;
-    return {M, L, make_float4(a.O.x * fa + b.O.x * fb, a.O.y * fa + b.O.y * fb, a.O.z * fa + b.O.z * fb, a.O.w * fa + b.O.w * fb)};
+
+// n of them, in the order of `get`: no step waits for another's exponential and quotient.
+template <class Get>
+__device__ __forceinline__ Joined join_all(int n, Get&& get) {
+    Joined r = {-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k = 0; k < n; ++k) r.M = fmaxf(r.M, get(k).M);
+    for (int k = 0; k < n; ++k) r.L = fmaf(get(k).L, ex2_approx(get(k).M - r.M), r.L);
+    const float inv = r.L == 0.f ? 0.f : __fdividef(1.f, r.L);
+    for (int k = 0; k < n; ++k) {
+        const Joined& a = get(k);
+        const float f = a.L * ex2_approx(a.M - r.M) * inv;
+        r.O = make_float4(fmaf(a.O.x, f, r.O.x), fmaf(a.O.y, f, r.O.y), fmaf(a.O.z, f, r.O.z), fmaf(a.O.w, f, r.O.w));
+    }
+    return r;
 }
 
 // A query head: its parts, the first one's slot (the others are the first slots of the following
@@ -914,19 +926,24 @@ __device__ __forceinline__ Joined join_parts(const CacheDecodeParams& p, const M
 
 // The groups of LPR lanes of a warp together: every lane gets the whole of its dims.
 template <int LPR>
-__device__ __forceinline__ Joined join_warp(Joined r) {
+__device__ __forceinline__ Joined join_warp(const Joined& r) {
+    float M = r.M;
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
+    const float l = r.L * ex2_approx(r.M - M);
+    float L = l;
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) L += __shfl_xor_sync(kFullMask, L, off);
+    const float f = L == 0.f ? 0.f : l * __fdividef(1.f, L);
+    float4 O = make_float4(r.O.x * f, r.O.y * f, r.O.z * f, r.O.w * f);
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
-        Joined o;
-        o.M = __shfl_xor_sync(kFullMask, r.M, off);
-        o.L = __shfl_xor_sync(kFullMask, r.L, off);
-        o.O.x = __shfl_xor_sync(kFullMask, r.O.x, off);
-        o.O.y = __shfl_xor_sync(kFullMask, r.O.y, off);
-        o.O.z = __shfl_xor_sync(kFullMask, r.O.z, off);
-        o.O.w = __shfl_xor_sync(kFullMask, r.O.w, off);
-        r = join(r, o);
+        O.x += __shfl_xor_sync(kFullMask, O.x, off);
+        O.y += __shfl_xor_sync(kFullMask, O.y, off);
+        O.z += __shfl_xor_sync(kFullMask, O.z, off);
+        O.w += __shfl_xor_sync(kFullMask, O.w, off);
     }
-    return r;
+    return {M, L, O};
 }
 
 __device__ __forceinline__ void write_joined(const CacheDecodeParams& p, bool q_bf16, const MergeHead& m, const Joined& r, int d) {
@@ -948,11 +965,7 @@ __global__ void __launch_bounds__(32 * WARPS) cache_decode_merge_head_kernel(con
     Joined r = join_warp<LPR>(join_parts<D, 4>(p, m, cols, threadIdx.x / LPR, 32 * WARPS / LPR, d));
     if (lane < LPR) joined[warp][lane] = r;
     __syncthreads();
-    if (threadIdx.x < LPR) {
-        r = joined[0][threadIdx.x];
-        for (int w = 1; w < WARPS; ++w) r = join(r, joined[w][threadIdx.x]);
-        write_joined(p, q_bf16, m, r, d);
-    }
+    if (threadIdx.x < LPR) write_joined(p, q_bf16, m, join_all(WARPS, [&](int w) -> const Joined& { return joined[w][threadIdx.x]; }), d);
 }
 
 // A CTA for all the query heads of a (sequence, kv head, block of columns): a thread joins four dims
@@ -979,7 +992,7 @@ __global__ void __launch_bounds__(kBlockThreads) cache_decode_merge_block_kernel
         if (groups > 1) {
             joined[threadIdx.x] = r;
             __syncthreads();
-            for (int k = 1; grp == 0 && k < groups; ++k) r = join(r, joined[k * items + i]);
+            if (grp == 0) r = join_all(groups, [&](int k) -> const Joined& { return joined[k * items + i]; });
         }
         if (i < items && grp == 0) write_joined(p, q_bf16, m, r, d);
     }
