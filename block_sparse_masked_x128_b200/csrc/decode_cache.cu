@@ -31,12 +31,11 @@
 //   Softmax    l sums 2^(x_j - m) in fp32, and O sums w_j v_j with w_j = 2^(x_j - m); over 8-bit
 //              caches w_j code_j with w_j = 2^(x_j - m) (vscale_j u), u a power of two that takes
 //              the largest weight near 1, so neither sum depends on the size of the other's terms.
-//              For the product a weight becomes two 16-bit numbers (bf16 results over 8-bit caches:
-//              one fp16 number).  m is raised to the largest x_j so far, and u set by the
-//              largest x_j + log2 vscale_j, only when a weight exceeds 2^8 (bf16 caches: m to 8
-//              above the largest x_j, when one exceeds 1): most tiles need no reduction over the
-//              lanes, and a weight is held to 2^-11 of itself (two numbers: 2^-16 at least) or, in
-//              fp16, 2^-25 of the largest, however the v scales differ.
+//              For the product a weight becomes two 16-bit numbers.  m is raised to the largest x_j
+//              so far, and u set by the largest x_j + log2 vscale_j, only when a weight exceeds 2^8
+//              (bf16 caches: m to 8 above the largest x_j, when one exceeds 1): most tiles need no
+//              reduction over the lanes, and a weight is held to 2^-16 (bf16) or 2^-22 of itself or,
+//              in fp16, 2^-25 of the largest, however the v scales differ.
 //
 // Measured (whole calls, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k tokens, bf16,
 // D = 128: 75 us, 6.15 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 234 us, 6.4 TB/s;
@@ -716,16 +715,13 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p) {
             }
 #pragma unroll
             for (int u = 0; u < C::sub; ++u) {
-                // The weights' transpose is the second operand.  For 16-bit caches, whose products have
-                // time to spare, a weight goes as two numbers, itself rounded and the rest: 8 bits of
-                // it in bf16 alone put the result's error at 1.3 times that of its own rounding.  A positive
-                // weight's first number is positive (fp16's least, 2^-24, at least; the rest, which may be
-                // negative, makes up for it) and alone meets infinite values, so that they stay infinite.
-                // Over 8-bit caches the second number is for fp16 results (error 3.0e-4 of their norm with one,
-                // 2.07e-4 with two); a bf16 result's own rounding is 8 times that of one number (grouped s8
-                // with two: 32.2 us, with one 31.0).
-                constexpr int PARTS = C::k8 && QBF ? 1 : 2;
-                uint32_t pb[PARTS][NT][2];
+                // The weights' transpose is the second operand.  A weight goes as two numbers, itself rounded
+                // and the rest, so that the result's error is that of its own rounding: one bf16 number makes
+                // it 1.3 times that, one fp16 number over 8-bit caches 1.5 times for fp16 results.  (The second
+                // costs a grouped s8 decode 31.0 -> 32.0 us, 16-bit caches nothing.)  Over 16-bit caches a
+                // positive weight's first number is positive (fp16's least, 2^-24, at least; the rest, which
+                // may be negative, makes up for it) and alone meets infinite values, so that they stay infinite.
+                uint32_t pb[2][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -735,10 +731,8 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p) {
                         auto first = [](float w) { return DT == FA_DTYPE_F16 && w > 0.f ? fmaxf(w, 0x1p-24f) : w; };
                         const uint32_t two = pack2<BF16>(first(w[u][nt][2 * i]), first(w[u][nt][2 * i + 1]));
                         pb[0][nt][i] = transpose8x8(two);
-                        if constexpr (PARTS == 2) {
-                            const float2 r2 = unpack2<BF16>(two);
-                            pb[1][nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i] - r2.x, w[u][nt][2 * i + 1] - r2.y));
-                        }
+                        const float2 r2 = unpack2<BF16>(two);
+                        pb[1][nt][i] = transpose8x8(pack2<BF16>(w[u][nt][2 * i] - r2.x, w[u][nt][2 * i + 1] - r2.y));
                     }
                 // O^T += V^T P^T: rows are dims, lane (r, c) holds D / 8 of them for its four keys.
                 const uint32_t vst = st + u * C::tile + C::kbytes;
@@ -765,7 +759,7 @@ cache_decode_kernel(const __grid_constant__ CacheDecodeParams p) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int k = 0; k < PARTS; ++k) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
+                                for (int k = 0; k < 2; ++k) mma16816<false>(o[nt][2 * q + hi], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
                         }
                 } else {
 #pragma unroll

@@ -419,7 +419,7 @@ fa_status_t fa_rotary(const fa_tensor_t* q, const fa_tensor_t* k, const int32_t*
  *   E4M3  scale = the smallest power of two >= 2^-126 with amax / scale <= 448,
  *         code = row / scale to the nearest even e4m3 value
  * with amax the row's largest magnitude.  A row with a NaN or an infinity is written with scale
- * NaN and codes 0.
+ * NaN and codes 0.  Scales that a caller writes are finite or NaN too.
  */
 typedef struct fa_kv_cache {
     void*   k;                 /* 16-byte aligned */

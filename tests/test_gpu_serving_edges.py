@@ -430,17 +430,18 @@ def test_decode_bad_pages_and_lengths_over_wide_tables(kind, D, B, H, G):
 @pytest.mark.parametrize("lens", [[1, 2, 5, 40, 700], [1, 2, 5, 40, 2500]], ids=["narrow", "wide"])
 @pytest.mark.parametrize("kind", ["s8", "e4m3"])
 @pytest.mark.parametrize("D, G", [(64, 3), (128, 12)])
-def test_decode_weights_over_8_bit_caches_for_fp16_results(kind, D, G, lens):
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+def test_decode_weights_over_8_bit_caches(kind, D, G, lens, dt):
     # Two fp16 numbers a weight: 2^-22 of itself, or 2^-25 of the largest where the second number is
-    # below fp16's normal range; then the result's one rounding, 2^-11 of it.
+    # below fp16's normal range; then the result's one rounding, half a step of it.
     fa = fa_module()
     cache, table, K, V = random_cache(kind, lens, 16, 2, D, seed=G)
-    q = rand((len(lens), 2 * G, 1, D), torch.float16, 9, 1.5)
+    q = rand((len(lens), 2 * G, 1, D), dt, 9, 1.5)
     out, lse = fa.decode_attention(q, cache, table, i32(*lens))
     for b, n in enumerate(lens):
         at = np.arange(n)
         vs = np64(cache.v_scale[table[b].long().cpu().numpy()[at // 16], :, at % 16]).T
         o, _, weight, reach, fine = ref.decode(np64(q[b, :, 0]), K[b], V[b], n, vscale=vs)
         score = D * 2.0 ** -24 * reach + 2e-6 * (1 + reach)              # a score's error, as everywhere
-        tol = 2.0 ** -11 * np.abs(o) + (2.0 ** -22 + 2 * score + 1e-5) * weight + 2.0 ** -25 * fine + 2.0 ** -25
+        tol = torch.finfo(dt).eps / 2 * np.abs(o) + (2.0 ** -22 + 2 * score + 1e-5) * weight + 2.0 ** -25 * fine + 2.0 ** -25
         assert (np.abs(np64(out[b, :, 0]) - o) <= tol).all()
