@@ -156,8 +156,8 @@ _lib.fa_backward.argtypes = [ctypes.POINTER(FaTensor)] * 5 + [
     ctypes.c_size_t, ctypes.c_void_p]
 _lib.fa_backward.restype = _status
 
-# The serving calls take their descriptions (fa_tensor_t, fa_kv_cache_t, ...) as addresses: a packed
-# bytes object or a byref() alike.
+# The serving calls take their descriptions (fa_tensor_t, fa_kv_cache_t, ...) as addresses; Python makes
+# them through the compiled binding, tests by byref().
 _p, _i64 = ctypes.c_void_p, ctypes.c_int64
 _lib.fa_rotary_frequencies.argtypes = [ctypes.c_int32, ctypes.c_double, _p, _p]
 _lib.fa_rotary.argtypes = [_p, _p, _p, _i64, _i64, _p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,

@@ -27,7 +27,8 @@
 //              the slots' order (below) is arranged.  No barrier between the warps.
 //   8 bits     codes become fp16 exactly, in registers.  The key's scale multiplies its score, the
 //              value's scale the weight, both in fp32.  q is brought into fp16's range by a power of
-//              two a head, so it keeps all its bits.
+//              two a head: its elements keep all their bits down to 2^-28 of the head's largest, and
+//              are off by 2^-39 of that below.
 //   Softmax    l sums 2^(x_j - m) in fp32, and O sums w_j v_j with w_j = 2^(x_j - m); over 8-bit
 //              caches w_j code_j with w_j = 2^(x_j - m) (vscale_j u), u a power of two that takes
 //              the largest weight near 1, so neither sum depends on the size of the other's terms.
@@ -37,10 +38,12 @@
 //              reduction over the lanes, and a weight is held to 2^-16 (bf16) or 2^-22 of itself or,
 //              in fp16, 2^-25 of the largest, however the v scales differ.
 //
-// Measured (whole calls, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k tokens, bf16,
-// D = 128: 75 us, 6.15 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 234 us, 6.4 TB/s;
-// one of 131072 tokens, 32 over 8 heads, e4m3: 52 us, 5.3 TB/s, of them 4 us the merge; one of 257
-// tokens, by a CTA a head: 4.4 us.  Without its arithmetic the kernel takes 2.4 us less at 8 bits, nothing less at 16.
+// Measured (calls replayed in a graph, B200, copy rate 6.57 TB/s): 16 sequences x 16 heads of 1k-8k
+// tokens, bf16, D = 128: 75 us, 6.1 TB/s; 96 sequences to 16384 tokens, 32 over 8 heads, bf16: 235 us,
+// 6.35 TB/s; one of 131072 tokens, 32 over 8 heads, e4m3: 52 us, 5.3 TB/s, of them 4 us the merge; 16 of
+// 1k-8k tokens, 64 over 8 heads, s8: 31 us; one of 257 tokens, by a CTA a head: 4.5 us.  Calls from
+// Python take 1 to 4 us more.  Without its arithmetic the kernel takes some 3 us less at 8 bits, nothing
+// less at 16.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
@@ -86,8 +89,8 @@ struct CdConfig {
     static constexpr int vbytes = 4 * vch * 32 * vb;      // 4 rows a lane
     static constexpr int tile = kbytes + vbytes + (k8 ? 128 : 0);
     // Tiles a warp works on at once: two independent chains of products and half the loop's
-    // overhead, where the ring has room for it (131072 tokens of e4m3: 52 us, with one tile 53.3
-    // at three CTAs an SM and 55.3 at four; with two CTAs and deeper rings 53.3).
+    // overhead, where the ring has room for it (131072 tokens of e4m3 in a graph, when it took 52 us
+    // too: with one tile 53.3 at three CTAs an SM and 55.3 at four; with two CTAs and deeper rings 53.3).
     static constexpr int sub = D * bytes == 256 ? 1 : 2;
     static constexpr int stage = sub * tile;
     static constexpr int occ = NT == 1 ? 3 : 2;
@@ -1024,9 +1027,10 @@ cudaError_t launch_split(CacheDecodeParams p, int nsm, cudaStream_t st) {
     static_assert(C::occ <= kMaxOcc, "the workspace counts kMaxOcc CTAs an SM");
     const int64_t blocks = (int64_t)p.B * p.c.H * col_blocks(p.group, 8 * NT);
     // Where the tables (or the window) leave few keys a head, a CTA each is faster than splitting and
-    // merging: up to 512 keys (8 sequences of 100-200 tokens, 32 over 8 heads: 4.8 us against 8.0; one
-    // of 500, 8 heads: 7.0 against 6.3, with a launch less), and up to 1024 where there is a head for
-    // every SM (32 of 500-1000: 20 against 23; with 16 heads in all 14.8 against 11.5).
+    // merging: up to 512 keys (in a graph, 8 sequences of 100-200 tokens, 32 over 8 heads: 4.8 us
+    // against 8.0; one of 500, 8 heads: 7.0 against 6.3, but outside a graph the split's second launch
+    // takes 2.4 us more of the host), and up to 1024 where there is a head for every SM (32 of 500-1000:
+    // 20 against 23; with 16 heads in all 14.8 against 11.5).
     const int keys = p.window > 0 ? std::min(p.window, p.c.capacity) : p.c.capacity;
     if (keys <= 512 || (keys <= 1024 && blocks >= nsm))
         return launch_kernel<DT, D, NT, true, QBF>(p, (unsigned)blocks, st);
@@ -1040,7 +1044,7 @@ cudaError_t launch_split(CacheDecodeParams p, int nsm, cudaStream_t st) {
     // The merge.  A head has workers / blocks parts on average, and what counts is how many loads
     // follow one another and how many CTAs start: few heads get four CTAs of 16 warps each, more get
     // four warps, and where heads are many, and their parts few, a CTA takes all the query heads of a
-    // kv head (whole calls: 1024 heads of 14 parts 30 us with four warps a head, 33 with one; 5824
+    // kv head (in a graph: 1024 heads of 14 parts 30 us with four warps a head, 33 with one; 5824
     // heads of one part 7.5 us by kv heads, 11.8 with four warps a query head).
     if (heads <= nsm)
         return launch_early(cache_decode_merge_head_kernel<D, 4, 16>, dim3((unsigned)heads, 4), dim3(512), 0, st, p, QBF, cols, sub);

@@ -8,12 +8,14 @@
 //          to the nearest even e4m3 value (the division is exact, so the code does not depend on
 //          the precision it is done in)
 // and a row that holds a NaN or an infinity gets scale = NaN, codes 0, and reads back as NaN.
-// 16-bit caches hold the rows as they are.  Reading gives code * scale rounded once.
+// 16-bit caches hold the rows as they are.  Reading gives code * scale in fp32 (exact for the scales that
+// e4m3 rows are written with, rounded for s8), rounded to 16 bits.
 //
 // Reading moves its bytes once and is bound by HBM (16 sequences of 1k-8k tokens, 16 heads, s8 to
-// bf16: 201 us for 1.31 GB, 0.99 of the copy rate).  Appending is bound by its instructions as much
-// (15k tokens of 8 heads to e4m3: 18 us for 95 MB; 16-bit magnitudes compared two at a time, 32-bit
-// positions and eight lanes a row took two thirds of them away).  A row belongs to eight or D / 8
+// bf16: 201 us in a graph for 1.31 GB, 0.99 of the copy rate).  Appending is bound by its instructions as
+// much (15k tokens of 8 heads to e4m3: 16.4 us in a graph for 95 MB; 16-bit magnitudes compared two at a
+// time, 32-bit positions and eight lanes a row took two thirds of them away; to s8, with its test for
+// quotients near a half, 22.9 us).  A row belongs to eight or D / 8
 // lanes, so its maximum is a few shuffles and nothing is staged; rows of k and v at the same place go
 // together.  The read has two rows of each in flight (four: 52.7 us against 49.6 for a prompt's write
 // and read).

@@ -8,14 +8,16 @@
 // taken of a 32-bit fraction in [-1/2, 1/2) turns.
 //
 // Bound by HBM (2 bytes read and 2 written an element): 40 heads x 32768 tokens of D = 128, half of
-// it turned, 115 us, 5.84 TB/s or 0.89 of the copy rate; 32 heads x 8192 tokens of D = 64, 13.1 us
-// with the launch.  A CTA takes a few tokens of every head: their cos and sin are computed once into
+// it turned, 115 us, 5.84 TB/s or 0.89 of the copy rate; 32 heads x 8192 tokens of D = 64, 13.2 us
+// (both replayed in a graph; calls 117 and 14.3).  A CTA takes a few tokens of every head: their cos and sin are computed once into
 // shared memory and serve all heads of q and k.  Work goes in columns of 16 bytes (half layout: the
 // two columns of eight pairs; of 8 bytes where rot_dim is a multiple of 8 but not of 16, the copied
 // rest in 16 all the same: 10 x 1833 tokens of 32 heads, 24 of 192 elements, 80 us, 107 before): a thread
 // keeps its column and walks the rows (token, head) by fixed offsets, with the loads of kAhead rows
 // in flight (twice as many: 20.5 us at 8192 tokens).  Pairs that do not fill such columns (half
-// layout with rot_dim no multiple of 8) go one by one.
+// layout with rot_dim no multiple of 8) go one by one: 26 of 64 elements at 8192 tokens take 83 us.
+// The table's arithmetic is shared by the heads, and where those are few it is what is waited for: 5
+// heads x 16384 tokens of D = 128, 12.8 us, half the copy rate.
 #include "serving.h"
 #include "sm100_ptx.cuh"
 
